@@ -381,6 +381,73 @@ int uno_tree_verify(const void* p_logits, const int32_t* node_token, const int32
                     int32_t* out_tokens, int32_t* accepted_len, void* stream);
 
 /* ------------------------------------------------------------------------ *
+ * RMS norm with the residual addition, and rows in 8-bit integers
+ *
+ * The pages' layers are those of a pre-norm decoder (summary page,
+ * "Methodology / Architecture"): each group of projections reads the RMS norm
+ * of the residual stream. These entry points write what the projections read,
+ * in the rows' own type (for uno_dualpath_linear) or as 8-bit integers with
+ * one scale per row (for uno_dualpath_linear_int8):
+ *   h = x + residual               rounded to dtype (residual NULL: h = x)
+ *   y = h / sqrt(mean(h^2) + eps) * w     float32, from the rounded h
+ *   scale = max|y| / 127,  q = y / scale rounded to nearest even, |q| <= 127
+ * uno_quantize_rows is the last line alone, for inputs that no norm writes
+ * (attention outputs, MLP activations). A row of zeros has scale 0 and q 0. A
+ * row with an infinity or NaN, or whose sum of squares passes float32, has
+ * scale NaN and q 0.
+ *
+ * x, residual  [M, d] dtype
+ * w            [d] dtype
+ * eps          >= 0, finite (else UNO_ERR_SIZE)
+ * M            0 <= M <= 2^24;  1 <= d <= 32768 (any d; multiples of 8 are faster)
+ * h            [M, d] dtype out, or NULL (may be x or residual itself)
+ * y            [M, d] dtype out, or NULL;  q [M, d] int8 out, or NULL (not both NULL)
+ * scale        [M] float out, required with q
+ * Row data 16-byte aligned. No workspace. Returns UNO_OK or a negative uno_status.
+ * ------------------------------------------------------------------------ */
+int uno_rms_norm(const void* x, const void* residual, const void* w, float eps, int M, int d,
+                 int dtype, void* h, void* y, int8_t* q, float* scale, void* stream);
+int uno_quantize_rows(const void* x, int M, int d, int dtype, int8_t* q, float* scale,
+                      void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * The paged 8-bit cache of keys and values, and its append
+ *
+ * Pages of `page` tokens: codes [num_pages, Hkv, page, D] (e4m3 bytes) and
+ * scales [num_pages, Hkv] float, one of each for keys and for values; a code
+ * stands for code * scale. Sequence b's token at position s is slot s % page
+ * of page page_table[b, s / page].
+ *
+ * uno_kv_append writes tokens j < count[b] of sequence b at positions
+ * start[b] + j: token j is row rows[b, j] (or j) of k_new / v_new. Per touched
+ * page and head the scale is the smallest power of two s >= 2^-126 with
+ * max|x| <= 448 s over the page's tokens so far (finite values only; 0 while
+ * all are zero); the codes are e4m3(x / s), rounded to nearest even, infinities
+ * to +-448, NaN kept. A page whose slot 0 is written starts afresh. Where
+ * a later token makes the scale grow, the page's earlier codes are written
+ * again at the new scale (exactly, but for codes that become subnormal).
+ * Nothing else is written: not slots behind the last appended token, not pages
+ * that are not touched. After a rejection the next append starts at the first
+ * rejected position; the page keeps the scale it has grown to.
+ *
+ * k_new, v_new  [B, T, Hkv, D] bf16
+ * start         [B] int32; a sequence with start < 0 or > width * page is skipped
+ * count         [B] int32, clamped to [0, n], or NULL: n tokens each
+ * rows          [B, n] int32 or NULL (then n <= T); the accepted path of a tree,
+ *               for example. An index outside [0, T) appends NaN.
+ * page_table    [B, width] int32; tokens on a page id outside [0, num_pages) or
+ *               past the table are not written. Pages that one call writes must
+ *               belong to one sequence each.
+ * Limits: 0 <= B <= 65535, 0 <= T, n <= 2^20, 1 <= Hkv <= 1024, D 64 or 128,
+ * page 16, 32, 64 or 128, width * page <= 2^30. k_new, v_new and the codes
+ * 16-byte aligned. No workspace. Asynchronous on `stream`.
+ * ------------------------------------------------------------------------ */
+int uno_kv_append(const void* k_new, const void* v_new, const int32_t* start,
+                  const int32_t* count, const int32_t* rows, int B, int T, int n, int Hkv, int D,
+                  int page, const int32_t* page_table, int width, int num_pages, void* k_codes,
+                  void* v_codes, float* k_scale, float* v_scale, void* stream);
+
+/* ------------------------------------------------------------------------ *
  * Device fault flags
  *
  * Every wait inside the kernels is bounded in time. A wait that gives up

@@ -86,6 +86,13 @@ def _load() -> ctypes.CDLL:
     L.uno_tree_verify.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, u64, u64, vp, vp,
                                   vp, vp]
     L.uno_tree_verify.restype = i32
+    L.uno_rms_norm.argtypes = [vp, vp, vp, ctypes.c_float, i32, i32, i32, vp, vp, vp, vp, vp]
+    L.uno_rms_norm.restype = i32
+    L.uno_quantize_rows.argtypes = [vp, i32, i32, i32, vp, vp, vp]
+    L.uno_quantize_rows.restype = i32
+    L.uno_kv_append.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, i32, i32,
+                                vp, vp, vp, vp, vp]
+    L.uno_kv_append.restype = i32
     L.uno_device_fault_flags.argtypes = [i32, ctypes.POINTER(ctypes.c_uint)]
     L.uno_device_fault_flags.restype = i32
     L.uno_dualpath_test_hooks.argtypes = [u64, ctypes.c_uint32]

@@ -529,6 +529,168 @@ def tree_verify(p_logits: torch.Tensor, tree: DraftTree, seed: int, step: int, *
     return out
 
 
+# ---------------------------------------------------------------------------
+# RMS norm and 8-bit rows
+# ---------------------------------------------------------------------------
+
+
+class _NoSwitch:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NO_SWITCH = _NoSwitch()
+
+
+def _on(dev: torch.device):
+    """Context in which `dev` is the current device (the C entry points launch there)."""
+    return _NO_SWITCH if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _expect(name: str, t: Optional[torch.Tensor], shape: tuple, dtype: torch.dtype) -> None:
+    if t is None:
+        return
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+@dataclass
+class RmsNormResult:
+    h: torch.Tensor                # [M, d] x + residual (x itself without a residual)
+    y: Optional[torch.Tensor]      # [M, d] the normed rows, in x's dtype
+    q: Optional[torch.Tensor]      # [M, d] int8, the normed rows in 8 bits
+    scale: Optional[torch.Tensor]  # [M] float32: a value is q * scale
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, *,
+             residual: Optional[torch.Tensor] = None, want_y: bool = False,
+             want_q: bool = True) -> RmsNormResult:
+    """h = x + residual and the RMS norm of h, as 8-bit rows with scales (q,
+    scale; for ``dualpath_linear_int8``) and / or in x's dtype (y; for
+    ``dualpath_linear``). See ``uno_rms_norm`` in uno.h. x, residual [M, d] and
+    weight [d] share a dtype (bfloat16 or float32); d <= 32768.
+    """
+    if x.dim() != 2:
+        raise ValueError("x must be [M, d]")
+    if not (want_y or want_q):
+        raise ValueError("want_y or want_q must be set")
+    M, d = x.shape
+    dt = _dtype_code(x)
+    _expect("weight", weight, (d,), x.dtype)
+    _expect("residual", residual, (M, d), x.dtype)
+    dev = _check_cuda(x, weight, residual)
+    with _on(dev):
+        h = x if residual is None else torch.empty_like(x)
+        y = torch.empty_like(x) if want_y else None
+        q = torch.empty((M, d), dtype=torch.int8, device=dev) if want_q else None
+        scale = torch.empty((M,), dtype=torch.float32, device=dev) if want_q else None
+        st = lib.uno_rms_norm(_ptr(x), _ptr(residual), _ptr(weight), float(eps), M, d, dt,
+                              None if residual is None else _ptr(h), _ptr(y), _ptr(q),
+                              _ptr(scale), _stream_handle(dev))
+    if st != 0:
+        raise UnoError(st, "uno_rms_norm")
+    return RmsNormResult(h, y, q, scale)
+
+
+def quantize_rows(x: torch.Tensor):
+    """8-bit integers and one float32 scale per row: x [M, d] (bfloat16 or
+    float32, d <= 32768) to (q [M, d] int8, scale [M]) with x ~ q * scale. Serves
+    activations that no norm writes, and lays out weights once (one scale per
+    output channel of a [d_out, d_in] weight)."""
+    if x.dim() != 2:
+        raise ValueError("x must be [M, d]")
+    M, d = x.shape
+    dt = _dtype_code(x)
+    dev = _check_cuda(x)
+    with _on(dev):
+        q = torch.empty((M, d), dtype=torch.int8, device=dev)
+        scale = torch.empty((M,), dtype=torch.float32, device=dev)
+        st = lib.uno_quantize_rows(_ptr(x), M, d, dt, _ptr(q), _ptr(scale), _stream_handle(dev))
+    if st != 0:
+        raise UnoError(st, "uno_quantize_rows")
+    return q, scale
+
+
+# ---------------------------------------------------------------------------
+# paged 8-bit cache
+# ---------------------------------------------------------------------------
+
+
+@dataclass
+class KvCache:
+    """A paged cache of keys and values in 8 bits (see ``uno_kv_append`` in uno.h)."""
+
+    k: torch.Tensor           # [num_pages, Hkv, page, D] float8_e4m3fn codes
+    v: torch.Tensor           # [num_pages, Hkv, page, D]
+    k_scale: torch.Tensor     # [num_pages, Hkv] float32: a key is code * scale
+    v_scale: torch.Tensor     # [num_pages, Hkv]
+    page_table: torch.Tensor  # [B, width] int32 page ids
+
+
+def kv_cache(page_table: torch.Tensor, num_pages: int, kv_heads: int, page: int,
+             head_dim: int) -> KvCache:
+    """An empty cache of num_pages pages of `page` tokens behind a page table [B, width]."""
+    if page not in (16, 32, 64, 128) or head_dim not in (64, 128):
+        raise ValueError("page must be 16, 32, 64 or 128 and head_dim 64 or 128")
+    dev = _check_cuda(page_table)
+    shape = (num_pages, kv_heads, page, head_dim)
+    codes = [torch.zeros(shape, dtype=torch.float8_e4m3fn, device=dev) for _ in range(2)]
+    scales = [torch.zeros(shape[:2], dtype=torch.float32, device=dev) for _ in range(2)]
+    return KvCache(*codes, *scales, page_table)
+
+
+def _check_cache(c: KvCache, B: int, Hkv: int, D: int) -> None:
+    if c.k.dim() != 4 or c.page_table.dim() != 2:
+        raise ValueError("cache codes must be [num_pages, Hkv, page, D], page_table [B, width]")
+    N, H, page, d = c.k.shape
+    if H != Hkv or d != D:
+        raise ValueError(f"cache holds {H} heads of {d}, the new rows {Hkv} of {D}")
+    _expect("cache.k", c.k, (N, Hkv, page, D), torch.float8_e4m3fn)
+    _expect("cache.v", c.v, (N, Hkv, page, D), torch.float8_e4m3fn)
+    _expect("cache.k_scale", c.k_scale, (N, Hkv), torch.float32)
+    _expect("cache.v_scale", c.v_scale, (N, Hkv), torch.float32)
+    _expect("cache.page_table", c.page_table, (B, c.page_table.shape[1]), torch.int32)
+
+
+def kv_append(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, start: torch.Tensor, *,
+              count: Optional[torch.Tensor] = None, rows: Optional[torch.Tensor] = None) -> None:
+    """Append rows of k_new, v_new [B, T, Hkv, D] (bfloat16) to a cache, in place.
+
+    Token j < count[b] of sequence b goes to position start[b] + j; it is row j
+    of the new rows, or row rows[b, j] (rows [B, n] int32: the accepted path of a
+    tree). start and count are int32 [B] on the device; count defaults to all.
+    """
+    if k_new.dim() != 4:
+        raise ValueError("k_new and v_new must be [B, T, Hkv, D]")
+    B, T, Hkv, D = k_new.shape
+    _expect("k_new", k_new, (B, T, Hkv, D), torch.bfloat16)
+    _expect("v_new", v_new, (B, T, Hkv, D), torch.bfloat16)
+    _expect("start", start, (B,), torch.int32)
+    _expect("count", count, (B,), torch.int32)
+    n = T
+    if rows is not None:
+        if rows.dim() != 2:
+            raise ValueError("rows must be [B, n]")
+        n = rows.shape[1]
+        _expect("rows", rows, (B, n), torch.int32)
+    _check_cache(cache, B, Hkv, D)
+    dev = _check_cuda(k_new, v_new, start, count, rows, cache.k, cache.v, cache.k_scale,
+                      cache.v_scale, cache.page_table)
+    with _on(dev):
+        st = lib.uno_kv_append(_ptr(k_new), _ptr(v_new), _ptr(start), _ptr(count), _ptr(rows), B,
+                               T, n, Hkv, D, cache.k.shape[2], _ptr(cache.page_table),
+                               cache.page_table.shape[1], cache.k.shape[0], _ptr(cache.k),
+                               _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale),
+                               _stream_handle(dev))
+    if st != 0:
+        raise UnoError(st, "uno_kv_append")
+
+
 def device_fault_flags(clear: bool = True) -> int:
     """Fault bits set by a kernel wait that gave up (0 = none). Synchronises."""
     flags = ctypes.c_uint(0)

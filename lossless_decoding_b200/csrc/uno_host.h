@@ -34,4 +34,13 @@ struct RowDraws {
 };
 int sample_rows(const RowDraws& r, cudaStream_t st);
 
+// Sizes of a paged 8-bit cache and of the B x T new rows that meet it, as
+// uno_kv_append and uno_block_attention accept them. Positions stay below 2^30,
+// so that sums of a position and a page stay in 32 bits.
+inline bool cache_sizes_ok(int B, int T, int Hkv, int D, int page, int width, int num_pages) {
+  return B >= 0 && B <= 65535 && T >= 0 && T <= (1 << 20) && Hkv >= 1 && Hkv <= 1024 &&
+         (D == 64 || D == 128) && (page == 16 || page == 32 || page == 64 || page == 128) &&
+         width >= 0 && width <= (1 << 30) / page && num_pages >= 0;
+}
+
 }  // namespace uno_host

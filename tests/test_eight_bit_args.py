@@ -1,0 +1,64 @@
+"""Argument checks of the 8-bit entry points (host side, no GPU)."""
+
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from lossless_decoding_b200.build import build_library
+    build_library()
+    from lossless_decoding_b200._lib import lib as L
+    return L
+
+
+FAKE, ODD = ctypes.c_void_p(4096), ctypes.c_void_p(4098)
+
+
+def _name(st):
+    from lossless_decoding_b200._lib import STATUS
+    return STATUS[st]
+
+
+def test_rms_norm_args(lib):
+    def call(x=FAKE, w=FAKE, eps=1e-6, M=4, d=64, dtype=0, h=None, y=None, q=FAKE, scale=FAKE):
+        return _name(lib.uno_rms_norm(x, None, w, eps, M, d, dtype, h, y, q, scale, None))
+
+    assert call(dtype=2) == "UNO_ERR_DTYPE"
+    assert call(M=-1) == call(d=0) == call(d=32769) == call(M=(1 << 24) + 1) == "UNO_ERR_SIZE"
+    assert call(eps=-1.0) == call(eps=float("nan")) == call(eps=float("inf")) == "UNO_ERR_SIZE"
+    assert call(x=None) == call(w=None) == call(q=None) == call(scale=None) == "UNO_ERR_NULL"
+    assert call(x=ODD) == call(w=ODD) == call(q=ODD) == call(y=ODD) == "UNO_ERR_ALIGN"
+    assert call(M=0, x=None, w=None, q=None, scale=None) == "UNO_OK"
+
+
+def test_quantize_rows_args(lib):
+    def call(x=FAKE, M=4, d=64, dtype=0, q=FAKE, scale=FAKE):
+        return _name(lib.uno_quantize_rows(x, M, d, dtype, q, scale, None))
+
+    assert call(dtype=-1) == "UNO_ERR_DTYPE"
+    assert call(d=0) == call(d=40000) == "UNO_ERR_SIZE"
+    assert call(x=None) == call(q=None) == call(scale=None) == "UNO_ERR_NULL"
+    assert call(x=ODD) == call(q=ODD) == "UNO_ERR_ALIGN"
+    assert call(M=0, x=None, q=None, scale=None) == "UNO_OK"
+
+
+def test_kv_append_args(lib):
+    def call(k=FAKE, start=FAKE, count=None, rows=None, B=2, T=4, n=4, H=2, D=64, page=16,
+             table=FAKE, width=3, N=6, codes=FAKE, scale=FAKE):
+        return _name(lib.uno_kv_append(k, FAKE, start, count, rows, B, T, n, H, D, page, table,
+                                       width, N, codes, FAKE, scale, FAKE, None))
+
+    for bad in (dict(B=-1), dict(B=65536), dict(T=-1), dict(n=-1), dict(n=5), dict(H=0),
+                dict(H=1025), dict(D=96), dict(page=48), dict(width=-1), dict(N=-1),
+                dict(width=1 << 27), dict(T=(1 << 20) + 1), dict(rows=FAKE, n=(1 << 20) + 1),
+                dict(B=65535, T=1 << 20, n=1 << 20, page=16)):
+        assert call(**bad) == "UNO_ERR_SIZE", bad
+    for bad in (dict(k=None), dict(start=None), dict(table=None), dict(codes=None),
+                dict(scale=None)):
+        assert call(**bad) == "UNO_ERR_NULL", bad
+    for bad in (dict(k=ODD), dict(codes=ODD), dict(start=ODD), dict(count=ODD), dict(rows=ODD),
+                dict(table=ODD), dict(scale=ODD)):
+        assert call(**bad) == "UNO_ERR_ALIGN", bad
+    assert call(B=0, k=None) == call(T=0, n=0, k=None) == "UNO_OK"
