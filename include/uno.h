@@ -411,6 +411,35 @@ int uno_quantize_rows(const void* x, int M, int d, int dtype, int8_t* q, float* 
                       void* stream);
 
 /* ------------------------------------------------------------------------ *
+ * Dual-pathway linear on 8-bit integers
+ *
+ * The dual-pathway linear above with x, the frozen W and the LoRA A held as
+ * int8 with a float32 scale per row of each (per token, per output channel,
+ * per rank row; uno_rms_norm and uno_quantize_rows write such rows):
+ *   y_ar    = x_scale[m] w_scale[n] sum_k x[m,k] W[n,k]
+ *   T       = scale x_scale[m] a_scale[j] sum_k x[m,k] A[j,k]   rounded to bf16
+ *   y_draft = y_ar + T Bm^T                                   (rows with gate 0: y_ar)
+ * The integer sums are exact (tcgen05 kind::i8, int32); they are scaled in
+ * float32, T Bm^T accumulates in float32 onto the unrounded y_ar, and outputs
+ * are rounded once to out_dtype.
+ *
+ * x [M, d_in], W [d_out, d_in], A [r, d_in] int8; x_scale [M], w_scale
+ * [d_out], a_scale [r] float; Bm [d_out, r] bf16; gate [M] uint8 or NULL;
+ * y_ar, y_draft [M, d_out] out_dtype (UNO_BF16 or UNO_F32), either NULL to skip
+ * it (y_draft NULL: A, a_scale and Bm are not read, r may be 0).
+ * Limits: 0 <= M <= 2^24; 16 <= d_in <= 65536, a multiple of 16; 1 <= d_out <=
+ * 2^24 (any; multiples of 8 are faster); r a multiple of 8, <= 256. Every
+ * pointer but gate 16-byte aligned. Workspace as for uno_dualpath_linear, at
+ * least uno_dualpath_int8_workspace_bytes(...) bytes (the same r as the call).
+ * ------------------------------------------------------------------------ */
+size_t uno_dualpath_int8_workspace_bytes(int M, int d_in, int d_out, int r);
+int uno_dualpath_linear_int8(const int8_t* x, const float* x_scale, const int8_t* W,
+                             const float* w_scale, const int8_t* A, const float* a_scale,
+                             const void* Bm, float scale, const uint8_t* gate, void* y_ar,
+                             void* y_draft, int M, int d_in, int d_out, int r, int out_dtype,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ *
  * The paged 8-bit cache of keys and values, and its append
  *
  * Pages of `page` tokens: codes [num_pages, Hkv, page, D] (e4m3 bytes) and

@@ -90,6 +90,11 @@ def _load() -> ctypes.CDLL:
     L.uno_rms_norm.restype = i32
     L.uno_quantize_rows.argtypes = [vp, i32, i32, i32, vp, vp, vp]
     L.uno_quantize_rows.restype = i32
+    L.uno_dualpath_int8_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    L.uno_dualpath_int8_workspace_bytes.restype = sz
+    L.uno_dualpath_linear_int8.argtypes = [vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp,
+                                           i32, i32, i32, i32, i32, vp, sz, vp]
+    L.uno_dualpath_linear_int8.restype = i32
     L.uno_kv_append.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, i32, i32,
                                 vp, vp, vp, vp, vp]
     L.uno_kv_append.restype = i32

@@ -616,6 +616,68 @@ def quantize_rows(x: torch.Tensor):
     return q, scale
 
 
+def dualpath_linear_int8(xq: torch.Tensor, x_scale: torch.Tensor, Wq: torch.Tensor,
+                         w_scale: torch.Tensor, Aq: Optional[torch.Tensor] = None,
+                         a_scale: Optional[torch.Tensor] = None,
+                         Bm: Optional[torch.Tensor] = None, scale: float = 1.0, *,
+                         gate: Optional[torch.Tensor] = None, want_ar: bool = True,
+                         out_dtype: torch.dtype = torch.bfloat16,
+                         workspace: Optional[torch.Tensor] = None):
+    """``dualpath_linear`` on 8-bit integers (see ``uno_dualpath_linear_int8`` in uno.h).
+
+    xq [M, d_in], Wq [d_out, d_in] and Aq [r, d_in] int8 with float32 scales per
+    row (x_scale [M], w_scale [d_out], a_scale [r]); Bm [d_out, r] bfloat16;
+    outputs [M, d_out] in out_dtype (bfloat16 or float32). Without an adapter
+    (Aq, a_scale and Bm None) y_draft is None. gate [M] (uint8/bool): rows with
+    gate 0 get no adapter. d_in is a multiple of 16, r of 8; M and d_out are any.
+    Returns (y_ar, y_draft).
+    """
+    if xq.dim() != 2 or Wq.dim() != 2:
+        raise ValueError("expected 2-D xq, Wq")
+    M, d_in = xq.shape
+    d_out = Wq.shape[0]
+    if out_dtype not in _DT:
+        raise TypeError(f"unsupported out_dtype {out_dtype}; use bfloat16 or float32")
+    adapter = Bm is not None
+    if (Aq is not None) != adapter or (a_scale is not None) != adapter:
+        raise ValueError("an adapter needs all of Aq, a_scale and Bm")
+    if not (adapter or want_ar):
+        raise ValueError("nothing to compute: no adapter and want_ar is False")
+    if gate is not None and not adapter:
+        raise ValueError("gate needs an adapter")
+    _expect("xq", xq, (M, d_in), torch.int8)
+    _expect("Wq", Wq, (d_out, d_in), torch.int8)
+    _expect("x_scale", x_scale, (M,), torch.float32)
+    _expect("w_scale", w_scale, (d_out,), torch.float32)
+    r = 0
+    if adapter:
+        if Aq.dim() != 2:
+            raise ValueError("expected 2-D Aq")
+        r = Aq.shape[0]
+        _expect("Aq", Aq, (r, d_in), torch.int8)
+        _expect("a_scale", a_scale, (r,), torch.float32)
+        _expect("Bm", Bm, (d_out, r), torch.bfloat16)
+        if r == 0:
+            raise ValueError("adapter rank must be at least 8")
+    dev = _check_cuda(xq, x_scale, Wq, w_scale, Aq, a_scale, Bm, workspace)
+    with _on(dev):
+        y_ar = torch.empty((M, d_out), dtype=out_dtype, device=dev) if want_ar else None
+        y_draft = torch.empty((M, d_out), dtype=out_dtype, device=dev) if adapter else None
+        if workspace is None:
+            # one of its own per call: calls on other streams, or replays of
+            # captured ones, never meet in it
+            need = int(lib.uno_dualpath_int8_workspace_bytes(M, d_in, d_out, r))
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        st = lib.uno_dualpath_linear_int8(
+            _ptr(xq), _ptr(x_scale), _ptr(Wq), _ptr(w_scale), _ptr(Aq), _ptr(a_scale), _ptr(Bm),
+            float(scale), _gate_arg(gate, M, dev), _ptr(y_ar), _ptr(y_draft), M, d_in, d_out, r,
+            _DT[out_dtype], _ptr(workspace), workspace.numel() * workspace.element_size(),
+            _stream_handle(dev))
+    if st != 0:
+        raise UnoError(st, "uno_dualpath_linear_int8")
+    return y_ar, y_draft
+
+
 # ---------------------------------------------------------------------------
 # paged 8-bit cache
 # ---------------------------------------------------------------------------

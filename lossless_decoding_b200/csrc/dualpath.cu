@@ -34,6 +34,15 @@
 // later than any CTA that waits for them; the wait is bounded and reports
 // through the fault flags.
 //
+// 8-bit integers (x, W and A int8 with a scale per row of each, Bm bf16): the
+// T tiles and main tiles accumulate x W^T and x A^T exactly in int32 (kind::i8).
+// T is rounded to bf16 with its scales applied, so that the adapter product is
+// a bf16 one; it cannot accumulate onto int32, so the epilogue's y_ar drain
+// writes the scaled float32 values back over the accumulator, and T Bm^T then
+// accumulates onto them as in the other types (a second accumulator for it
+// would take the TMEM columns that let the next tile's products overlap the
+// drain).
+//
 // For M <= 256 the operands swap roles (W rows fill the 128-row MMA side, the
 // few activation rows are the N side), so small-batch decode still runs at full
 // tile height while it is bound by the stream of W.
@@ -45,6 +54,7 @@
 #include <cstring>
 #include <initializer_list>
 #include <mutex>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -85,6 +95,8 @@ struct GroupArgs {
   float scale;        // alpha / r
   void* y_ar;         // may be null
   void* y_draft;      // may be null (then for every projection)
+  const float* w_scale;  // [ncols] scale per output channel (int8 only)
+  const float* a_scale;  // [r] scale per row of the LoRA A (int8 only)
   void* t_buf;        // T [M][r]
   uint32_t* t_flags;  // [nT]
   float2* stats_ar;     // [M][stats_tiles] row softmax partials of y_ar (may be null)
@@ -117,6 +129,7 @@ struct GemmParams {
   uint32_t* part_flags;  // [n_split][split_k - 1]
   size_t part_capacity;  // bytes available at part_buf (host side: decides the split)
   const uint8_t* gate;   // [M] per-row adapter gate (0: AR only), or null (all on)
+  const float* x_scale;  // [M] scale per row of x (int8 only)
   GroupArgs g[kMaxGroups];
 };
 
@@ -200,10 +213,26 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
-// Store 32 consecutive columns of one output row (valid_cols of them exist).
 template <typename T>
-__device__ __forceinline__ void store_row32(T* dst, const float* v, int valid_cols) {
+__device__ __forceinline__ void store_one(T* dst, float v) {
   if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xFFFFu);
+  } else {
+    *dst = v;
+  }
+}
+
+// Store 32 consecutive columns of one output row (valid_cols of them exist);
+// `whole`: rows are a multiple of 16 bytes long, so 16-byte pieces are aligned
+// and exist as a whole.
+template <typename T>
+__device__ __forceinline__ void store_row32(T* dst, const float* v, int valid_cols,
+                                            bool whole = true) {
+  if (!whole) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (e < valid_cols) store_one<T>(dst + e, v[e]);
+  } else if constexpr (sizeof(T) == 2) {
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       if (g * 8 < valid_cols) {
@@ -225,12 +254,15 @@ __device__ __forceinline__ void store_row32(T* dst, const float* v, int valid_co
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void store_one(T* dst, float v) {
-  if constexpr (sizeof(T) == 2) {
-    *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xFFFFu);
+// 32 scales of rows or columns at..at+31 (0 past n), 16-byte loads where they all exist.
+__device__ __forceinline__ void load_scales32(const float* s, int at, int n, float* out) {
+  if (at + 32 <= n) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      reinterpret_cast<float4*>(out)[e] = __ldg(reinterpret_cast<const float4*>(s + at) + e);
   } else {
-    *dst = v;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) out[e] = at + e < n ? __ldg(s + at + e) : 0.f;
   }
 }
 
@@ -385,6 +417,15 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
   }
 }
 
+__device__ __forceinline__ void mma_pair_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+
 // Arrive on `bar` (same offset) in both CTAs of the pair once the issuing
 // thread's MMAs have completed.
 __device__ __forceinline__ void commit_pair(uint64_t* bar) {
@@ -412,8 +453,9 @@ __device__ bool wait_flag(const uint32_t* flag, uint32_t epoch, uint64_t limit_n
 // T tiles: x and the LoRA down weight A (unswapped: A on the B side, swapped:
 // on the A side). Every projection of a grouped launch has its own W, Bm, T,
 // A and outputs; x is shared.
+// T: operand type (int8_t: x, W and A; T and Bm are bf16); Y: output type.
 // ---------------------------------------------------------------------------
-template <typename T, int BN, bool SWAP, bool PAIR>
+template <typename T, typename Y, int BN, bool SWAP, bool PAIR>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     dual_kernel(const __grid_constant__ DualMaps m, const __grid_constant__ GemmParams p) {
   static_assert(!(PAIR && SWAP), "the CTA pair serves the unswapped layout");
@@ -424,9 +466,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   constexpr int kKb = kblock_bytes<BN, PAIR>();   // bytes of one K-block in a stage
   constexpr int kStage = stage_bytes<BN, PAIR>();
   constexpr int kRows = PAIR ? 2 * kBM : kBM;  // output rows of a tile (both CTAs)
+  constexpr bool kI8 = sizeof(T) == 1;
   constexpr bool kTf32 = sizeof(T) == 4;
+  using Tt = std::conditional_t<kI8, uint16_t, T>;  // type of T and Bm
   constexpr int kElemsPerRow = kRowBytes / static_cast<int>(sizeof(T));
-  constexpr uint32_t kIdesc = sm100::instr_desc(kTf32, kRows, BN);
+  constexpr int kElemsPerRowT = kRowBytes / static_cast<int>(sizeof(Tt));
+  // main tiles, and their adapter product
+  constexpr uint32_t kIdesc =
+      kI8 ? sm100::instr_desc_i8(kRows, BN) : sm100::instr_desc(kTf32, kRows, BN);
+  constexpr uint32_t kIdescAd = sm100::instr_desc(kTf32, kRows, BN);
   constexpr int kEpiArrivals = PAIR ? 8 : 4;  // epilogue warps of the pair / the CTA
   constexpr int kAcc = pow2_at_least(BN);  // columns of one accumulator buffer
   constexpr uint32_t kTmemCols = 2 * kAcc;
@@ -716,7 +764,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           uint8_t* stage = begin_item(kBrows, nk);
           if (!stage) break;
           for (int jj = 0; jj < nk; ++jj) {
-            const int kx = (j * KBI + jj) * kElemsPerRow;
+            const int kx = (j * KBI + jj) * kElemsPerRowT;
             if constexpr (SWAP)
               load_kb(stage, jj, &m.bm[owner.g], owner.a0, &m.t[owner.g], owner.b0, kx);
             else
@@ -755,8 +803,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         else sm100::mma_commit(bar);
       };
       // The MMAs of ring item `it` (nk K-blocks of 4 MMAs each); the first
-      // MMA overwrites the accumulator unless accumulate_first.
-      auto issue = [&](uint32_t d, uint32_t idesc, bool accumulate_first, int nk) {
+      // MMA overwrites the accumulator unless accumulate_first. adapter_item:
+      // an item of T and Bm (their own type where x and W are int8).
+      auto issue = [&](uint32_t d, uint32_t idesc, bool accumulate_first, int nk,
+                       bool adapter_item) {
         const int s = it % STAGES;
         if (!wait_order(order, it, &abort_flag, p.wait_ns) ||
             !sm100::mbar_wait(&full_bar[s], (it / STAGES) & 1, p.wait_ns)) {
@@ -773,6 +823,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const bool acc = accumulate_first || (jj > 0) || (k > 0);
+              if constexpr (kI8) {
+                if (!adapter_item) {
+                  if constexpr (PAIR) mma_pair_i8(d, da + 2 * k, db + 2 * k, idesc, acc);
+                  else sm100::mma_i8(d, da + 2 * k, db + 2 * k, idesc, acc);
+                  continue;
+                }
+              }
               if constexpr (PAIR)
                 mma_pair<kTf32>(d, da + 2 * k, db + 2 * k, idesc, acc);
               else
@@ -806,7 +863,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 sm100::tc_fence_after();
               }
               // adds T Bm^T onto y_ar of the previous tile
-              issue(pd, kIdesc, true, item_kbs(j, c.nprev));
+              issue(pd, kIdescAd, true, item_kbs(j, c.nprev), true);
             }
             if (ok && j == c.iprev - 1) commit(&draft_full[mo & 1]);
           } else if (kind == 2) {
@@ -819,7 +876,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
                 sm100::tc_fence_after();
               }
-              issue(pd, kIdesc, j > 0, item_kbs(j, c.nself));  // T Bm^T of this tile, on its own
+              issue(pd, kIdescAd, j > 0, item_kbs(j, c.nself), true);  // T Bm^T of this tile, on its own
             }
             if (ok && j == c.iself - 1) commit(&acc_full[buf]);
           } else {
@@ -831,7 +888,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
                 sm100::tc_fence_after();
               }
-              issue(d, idesc, j > 0, item_kbs(j, c.nmain));
+              issue(d, idesc, j > 0, item_kbs(j, c.nmain), false);
             }
             if (ok && j == c.imain - 1 && c.nself == 0) commit(&acc_full[buf]);
           }
@@ -904,17 +961,38 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       for (int q = 0; q < 2 * BN; q += 32)
         srs[quarter * 2 * BN + q + lane] = make_float2(-INFINITY, 0.f);
     // outputs of the projection of the tile being drained
-    T* ya = nullptr;
-    T* yd = nullptr;
-    T* tb = nullptr;
+    Y* ya = nullptr;
+    Y* yd = nullptr;
+    Tt* tb = nullptr;
     int ncols = 0, gi = 0;
+    // whether output rows are a multiple of 16 bytes (int8 takes any d_out)
+    bool whole = true;
+    // int8: 32 int32 accumulator columns (B rows brow..) as float32, times the
+    // scales of the A side's row (sa) and the B side's rows (sb[0..n_b)); each
+    // product is rounded once per factor.
+    auto scaled = [&](const uint32_t* v, float* f, float sa, const float* sb, int brow, int n_b) {
+      float s[32];
+      load_scales32(sb, brow, n_b, s);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) f[e] = static_cast<float>(static_cast<int>(v[e])) * sa * s[e];
+    };
+    // The A-side scale of this thread's row of a main tile, and the B side's.
+    auto side_a = [&](int arow) {
+      if constexpr (!kI8) return 1.f;
+      const float* s = SWAP ? p.g[gi].w_scale : p.x_scale;
+      return arow < (SWAP ? ncols : p.M) ? __ldg(s + arow) : 0.f;
+    };
     // Drain accumulator columns [0, ncol) into y (row-major, ld columns, nrows rows).
     // gate: for T tiles, the per-row adapter gate (rows of x: the A rows
     // unswapped, the B rows swapped); a closed row stores T = 0.
-    auto drain = [&](uint32_t acc, int a0, int b0, T* y, int ld, int nrows, int ncol,
+    // int8: the accumulator is int32 unless `from_f32`; sa and sb (n_b of them)
+    // are the scales of its sides, and `keep` writes the float32 values back.
+    auto drain = [&](uint32_t acc, int a0, int b0, auto* y, int ld, int nrows, int ncol,
                      float mul, const uint8_t* gate = nullptr, float2* stats = nullptr,
-                     int stats_tiles = 0, int stat_out = 0) {
-      if (!y) return;
+                     int stats_tiles = 0, int stat_out = 0, bool from_f32 = true, float sa = 1.f,
+                     const float* sb = nullptr, int n_b = 0, bool keep = false) {
+      using To = std::remove_pointer_t<decltype(y)>;
+      if (!y && !keep) return;
       const uint32_t tq = acc + (static_cast<uint32_t>(quarter * 32) << 16);
       const int arow = a0 + rr;
       if constexpr (!SWAP) {
@@ -927,9 +1005,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         sm100::tmem_ld_32x32b_x32(tq + c, v);
         sm100::tmem_ld_wait();
         float f[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]) * mul;
         const int brow = b0 + c;
+        if (kI8 && !from_f32) {
+          scaled(v, f, sa * mul, sb, brow, n_b);
+          if (keep) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(f[e]);
+            sm100::tmem_st_32x32b_x32(tq + c, v);
+          }
+          if (!y) continue;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]) * mul;
+        }
         if constexpr (SWAP) {
           if (gate) {
 #pragma unroll
@@ -940,11 +1028,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if constexpr (!SWAP) {
           // row = A row, column = B row
           if (arow < nrows && brow < ld)
-            store_row32<T>(y + static_cast<size_t>(arow) * ld + brow, f, ld - brow);
+            store_row32<To>(y + static_cast<size_t>(arow) * ld + brow, f, ld - brow,
+                            !kI8 || ld % (16 / static_cast<int>(sizeof(To))) == 0);
           if (stats && brow < ld) {
             float sv[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) sv[e] = stored_value<T>(f[e]);
+            for (int e = 0; e < 32; ++e) sv[e] = stored_value<To>(f[e]);
             rs.add(sv, min(32, ld - brow));
           }
         } else {
@@ -953,16 +1042,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (brow + e < nrows)
-                store_one<T>(y + static_cast<size_t>(brow + e) * ld + arow, f[e]);
+                store_one<To>(y + static_cast<size_t>(brow + e) * ld + arow, f[e]);
           }
           if (stats) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              f[e] = (arow < ld && brow + e < nrows) ? stored_value<T>(f[e]) : -INFINITY;
+              f[e] = (arow < ld && brow + e < nrows) ? stored_value<To>(f[e]) : -INFINITY;
             swap_row_stats(f, stat_out, c);
           }
         }
       }
+      if (kI8 && keep) sm100::tmem_st_wait();
       if constexpr (!SWAP) {
         if (stats && arow < nrows)
           stats[static_cast<size_t>(arow) * stats_tiles + b0 / BN] = make_float2(rs.m, rs.z);
@@ -984,11 +1074,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       RowStats rs_ar, rs_dr;
       rs_ar.init();
       rs_dr.init();
+      const float sa = side_a(a0 + lane);
       for (int c = 0; c < BN; c += 32) {
         uint32_t v[32], w[32];
         sm100::tmem_ld_32x32b_x32(acc + lq + c, v);
         sm100::tmem_ld_32x32b_x32(adp + lq + c, w);
         sm100::tmem_ld_wait();
+        if constexpr (kI8) {
+          float f[32];
+          scaled(v, f, sa, p.g[gi].w_scale, b0 + c, ncols);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(f[e]);
+        }
         // columns c..c+31 = 4 chunks of 16 bytes in box c/64, chunks (c%64)/8..+3
         float sva[32], svd[32];
         const int box = c >> 6;
@@ -1059,6 +1156,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       RowStats rs2[2];
       rs2[0].init();
       rs2[1].init();
+      const float sa = side_a(arow);
       for (int c = 0; c < BN; c += 32) {
         uint32_t v[32], w[32];
         sm100::tmem_ld_32x32b_x32(acc + lq + c, v);
@@ -1066,33 +1164,39 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         sm100::tmem_ld_wait();
         float f[32];
         const int brow = b0 + c;
+        if constexpr (kI8) {
+          if constexpr (SWAP) scaled(v, f, sa, p.x_scale, brow, p.M);
+          else scaled(v, f, sa, p.g[gi].w_scale, brow, ncols);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(f[e]);
+        }
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {
-          T* y = pass ? yd : ya;
+          Y* y = pass ? yd : ya;
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             f[e] = pass ? f[e] + __uint_as_float(w[e]) : __uint_as_float(v[e]);
           if (!y) continue;
           if constexpr (!SWAP) {
             if (arow < p.M && brow < ncols)
-              store_row32<T>(y + static_cast<size_t>(arow) * ncols + brow, f, ncols - brow);
+              store_row32<Y>(y + static_cast<size_t>(arow) * ncols + brow, f, ncols - brow, whole);
             if (st2[pass] && brow < ncols) {
               float sv[32];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) sv[e] = stored_value<T>(f[e]);
+              for (int e = 0; e < 32; ++e) sv[e] = stored_value<Y>(f[e]);
               rs2[pass].add(sv, min(32, ncols - brow));
             }
           } else {
             if (arow < ncols) {
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (brow + e < p.M) store_one<T>(y + static_cast<size_t>(brow + e) * ncols + arow, f[e]);
+                if (brow + e < p.M) store_one<Y>(y + static_cast<size_t>(brow + e) * ncols + arow, f[e]);
             }
             if (st2[pass]) {
               float sv[32];
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                sv[e] = (arow < ncols && brow + e < p.M) ? stored_value<T>(f[e]) : -INFINITY;
+                sv[e] = (arow < ncols && brow + e < p.M) ? stored_value<Y>(f[e]) : -INFINITY;
               swap_row_stats(sv, pass, c);
             }
           }
@@ -1118,15 +1222,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
       sm100::tc_fence_after();
       gi = x.g;
-      ya = static_cast<T*>(p.g[gi].y_ar);
-      yd = static_cast<T*>(p.g[gi].y_draft);
-      tb = static_cast<T*>(p.g[gi].t_buf);
+      ya = static_cast<Y*>(p.g[gi].y_ar);
+      yd = static_cast<Y*>(p.g[gi].y_draft);
+      tb = static_cast<Tt*>(p.g[gi].t_buf);
       ncols = p.g[gi].ncols;
+      if constexpr (kI8) whole = ncols % (16 / static_cast<int>(sizeof(Y))) == 0;
       if (x.is_t) {
         // T = scale * x A^T: non-swapped, rows of x by r columns; swapped, r
         // rows (rows of A) by the M columns of x.
-        if constexpr (!SWAP) drain(acc, x.a0 + my_rows, 0, tb, p.r, p.M, p.r, p.g[gi].scale, p.gate);
-        else drain(acc, x.a0, 0, tb, p.r, p.M, BN, p.g[gi].scale, p.gate);
+        if constexpr (!SWAP) {
+          const int arow = x.a0 + my_rows + rr;
+          drain(acc, x.a0 + my_rows, 0, tb, p.r, p.M, p.r, p.g[gi].scale, p.gate, nullptr, 0, 0,
+                !kI8, (kI8 && arow < p.M) ? __ldg(p.x_scale + arow) : 0.f, p.g[gi].a_scale, p.r);
+        } else {
+          const int arow = x.a0 + rr;
+          drain(acc, x.a0, 0, tb, p.r, p.M, BN, p.g[gi].scale, p.gate, nullptr, 0, 0, !kI8,
+                (kI8 && arow < p.r) ? __ldg(p.g[gi].a_scale + arow) : 0.f, p.x_scale, p.M);
+        }
         sm100::tc_fence_before();
         __threadfence();
         __syncwarp();
@@ -1197,6 +1309,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           if (lane == 0) set_fault(kFaultEpilogue, &abort_flag);
           break;
         }
+        // (int8: the partials are int32, carried as bits)
+        auto add_partial = [](uint32_t a, float b) {
+          if constexpr (kI8) return a + __float_as_uint(b);
+          else return __float_as_uint(__uint_as_float(a) + b);
+        };
         // every piece's loads of a 32-column chunk are issued before any is
         // used (up to 24 x 16 bytes in flight per thread: one L2 round trip
         // per chunk, not one per chunk and piece)
@@ -1218,10 +1335,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if (q < p.split_k) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                v[4 * e] = __float_as_uint(__uint_as_float(v[4 * e]) + f[q - 1][e].x);
-                v[4 * e + 1] = __float_as_uint(__uint_as_float(v[4 * e + 1]) + f[q - 1][e].y);
-                v[4 * e + 2] = __float_as_uint(__uint_as_float(v[4 * e + 2]) + f[q - 1][e].z);
-                v[4 * e + 3] = __float_as_uint(__uint_as_float(v[4 * e + 3]) + f[q - 1][e].w);
+                v[4 * e] = add_partial(v[4 * e], f[q - 1][e].x);
+                v[4 * e + 1] = add_partial(v[4 * e + 1], f[q - 1][e].y);
+                v[4 * e + 2] = add_partial(v[4 * e + 2], f[q - 1][e].z);
+                v[4 * e + 3] = add_partial(v[4 * e + 3], f[q - 1][e].w);
               }
             }
           sm100::tmem_st_32x32b_x32(acc + lq + c, v);
@@ -1230,15 +1347,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
       if (adapter && li == nmine - 1) {
         // last tile: y_ar in this buffer, T Bm^T in the other; one pass
-        if constexpr (PAIR && sizeof(T) == 2)
-          drain2_tma(acc, tmem + static_cast<uint32_t>((buf ^ 1) * kAcc),
-                     x.a0 + my_rows + quarter * 32, x.b0);
-        else
+        if constexpr (PAIR && sizeof(Y) == 2) {
+          if (whole)
+            drain2_tma(acc, tmem + static_cast<uint32_t>((buf ^ 1) * kAcc),
+                       x.a0 + my_rows + quarter * 32, x.b0);
+          else
+            drain2(acc, tmem + static_cast<uint32_t>((buf ^ 1) * kAcc), x.a0 + my_rows, x.b0);
+        } else {
           drain2(acc, tmem + static_cast<uint32_t>((buf ^ 1) * kAcc), x.a0 + my_rows, x.b0);
+        }
         break;
       }
       drain(acc, x.a0 + my_rows, x.b0, ya, ncols, p.M, BN, 1.f, nullptr, p.g[gi].stats_ar,
-            p.g[gi].stats_tiles, 0);
+            p.g[gi].stats_tiles, 0, !kI8, side_a(x.a0 + my_rows + rr),
+            SWAP ? p.x_scale : p.g[gi].w_scale, SWAP ? p.M : ncols, kI8 && adapter);
       sm100::tc_fence_before();
       __syncwarp();
       const int mo = li - nt_mine;
@@ -1315,12 +1437,16 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
   return fn;
 }
 
+constexpr int kInt8 = 2;  // operand type of uno_dualpath_linear_int8, beside the uno_dtype values
+
+int elem_size(int dtype) { return dtype == UNO_BF16 ? 2 : dtype == kInt8 ? 1 : 4; }
+
 // 2-D K-major map: inner dimension K (elements), outer dimension rows; box of
 // 128 bytes of K by box_rows rows, 128-byte swizzle, zero fill out of bounds.
 bool make_map(CUtensorMap* map, const void* ptr, int dtype, int k_elems, int rows, int box_rows) {
   auto enc = get_encode();
   if (!enc) return false;
-  const size_t esize = (dtype == UNO_BF16) ? 2 : 4;
+  const size_t esize = static_cast<size_t>(elem_size(dtype));
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(k_elems), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(k_elems) * esize};
   cuuint32_t box[2] = {static_cast<cuuint32_t>(kRowBytes / esize),
@@ -1328,6 +1454,7 @@ bool make_map(CUtensorMap* map, const void* ptr, int dtype, int k_elems, int row
   cuuint32_t estr[2] = {1, 1};
   const CUresult r = enc(map,
                          dtype == UNO_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                         : dtype == kInt8  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                          2, const_cast<void*>(ptr), dims, strides, box, estr,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -1413,10 +1540,10 @@ int max_pairs(K kern, int bytes) {
   return n;
 }
 
-template <typename T, int BN, bool SWAP, bool PAIR>
+template <typename T, typename Y, int BN, bool SWAP, bool PAIR>
 int launch_dual(const DualMaps& maps, const GemmParams& p, cudaStream_t st) {
   constexpr int bytes = smem_bytes<BN, PAIR>();
-  auto kern = dual_kernel<T, BN, SWAP, PAIR>;
+  auto kern = dual_kernel<T, Y, BN, SWAP, PAIR>;
   static std::atomic<uint64_t> attr_done{0};  // devices with the shared-memory opt-in
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return UNO_ERR_CUDA;
@@ -1494,18 +1621,21 @@ int launch_dual(const DualMaps& maps, const GemmParams& p, cudaStream_t st) {
   return (cudaGetLastError() == cudaSuccess) ? UNO_OK : UNO_ERR_CUDA;
 }
 
-template <typename T>
+template <typename T, typename Y = T>
 int launch_swapped(int bn, const DualMaps& maps, const GemmParams& p, cudaStream_t st) {
   switch (bn) {
-    case 32: return launch_dual<T, 32, true, false>(maps, p, st);
-    case 64: return launch_dual<T, 64, true, false>(maps, p, st);
-    case 128: return launch_dual<T, 128, true, false>(maps, p, st);
-    default: return launch_dual<T, 256, true, false>(maps, p, st);
+    case 32: return launch_dual<T, Y, 32, true, false>(maps, p, st);
+    case 64: return launch_dual<T, Y, 64, true, false>(maps, p, st);
+    case 128: return launch_dual<T, Y, 128, true, false>(maps, p, st);
+    default: return launch_dual<T, Y, 256, true, false>(maps, p, st);
   }
 }
 
 
 bool dual_sizes_ok(int M, int d_in, int d_out, int r, int dtype) {
+  if (dtype == kInt8)  // int32 sums of d_in products of at most 2^14
+    return M >= 0 && M <= (1 << 24) && d_in >= 1 && d_in <= (1 << 16) && d_in % 16 == 0 &&
+           d_out >= 1 && d_out <= (1 << 24) && r >= 1 && r <= 256 && r % 8 == 0;
   if (dtype != UNO_BF16 && dtype != UNO_F32) return false;
   const int q = (dtype == UNO_BF16) ? 8 : 4;
   return M >= 0 && M <= (1 << 24) && d_in >= 1 && d_out >= 1 && r >= 1 && r <= 256 &&
@@ -1513,7 +1643,7 @@ bool dual_sizes_ok(int M, int d_in, int d_out, int r, int dtype) {
          d_out <= (1 << 24);
 }
 
-// Per-projection workspace: T [M][r] in the operand type, then its T-tile flags.
+// Per-projection workspace: T [M][r] in the operand type (int8: bf16), then its T-tile flags.
 struct Plan {
   bool swap;
   int esize, kb_main, kb_adapt, nT;
@@ -1528,13 +1658,14 @@ constexpr int kSizingSms = 148;
 
 Plan make_plan(int M, int d_in, int r, int dtype) {
   Plan pl{};
-  pl.esize = (dtype == UNO_BF16) ? 2 : 4;
+  pl.esize = elem_size(dtype);
+  const int t_esize = dtype == kInt8 ? 2 : pl.esize;
   pl.swap = M <= 256;
   pl.kb_main = (d_in * pl.esize + kRowBytes - 1) / kRowBytes;
-  pl.kb_adapt = (r * pl.esize + kRowBytes - 1) / kRowBytes;
+  pl.kb_adapt = (r * t_esize + kRowBytes - 1) / kRowBytes;
   // with M > 256 a CTA pair computes 256-row tiles, so one T tile per 256 rows
   pl.nT = pl.swap ? (r + kBM - 1) / kBM : (M + 2 * kBM - 1) / (2 * kBM);
-  pl.t_bytes = align256(static_cast<size_t>(M) * r * pl.esize);
+  pl.t_bytes = align256(static_cast<size_t>(M) * r * t_esize);
   pl.flag_bytes = align256(static_cast<size_t>(pl.nT) * sizeof(uint32_t));
   const int bn = pl.swap ? bn_for(M) : 256;
   const size_t per_slot = static_cast<size_t>(pl.swap ? 1 : 2) * kBM * bn * sizeof(float);
@@ -1543,16 +1674,26 @@ Plan make_plan(int M, int d_in, int r, int dtype) {
   return pl;
 }
 
-template <typename T>
+// Scales of int8 operands: of x's rows, and per projection of W's and A's rows.
+struct Int8Scales {
+  const float* x;
+  const float* const* w;
+  const float* const* a;
+};
+
+template <typename T, typename Y = T>
 int run_dualpath(int n, const void* x, const void* const* W, const void* const* A,
                  const void* const* Bm, const float* scale, const uint8_t* gate,
                  void* const* y_ar, void* const* y_draft, int M, int d_in, const int* d_out,
                  int r, int dtype, void* workspace, cudaStream_t st,
-                 float* const* stats_ar = nullptr, float* const* stats_draft = nullptr) {
+                 float* const* stats_ar = nullptr, float* const* stats_draft = nullptr,
+                 const Int8Scales* i8 = nullptr) {
   const Plan pl = make_plan(M, d_in, r, dtype);
   const bool adapter = (y_draft[0] != nullptr);
   const bool tf32 = (dtype == UNO_F32);
+  const int t_dtype = i8 ? UNO_BF16 : dtype;  // of T and Bm
   GemmParams gp{};
+  gp.x_scale = i8 ? i8->x : nullptr;
   gp.kb_total = pl.kb_main;
   gp.nkb_adapt = adapter ? pl.kb_adapt : 0;
   gp.M = M;
@@ -1570,7 +1711,8 @@ int run_dualpath(int n, const void* x, const void* const* W, const void* const* 
   }
   DualMaps maps;
   const int bn = pl.swap ? bn_for(M) : 256;
-  const int n_t = (r + 15) / 16 * 16;  // N of the unswapped T tiles
+  // N of the unswapped T tiles (a pair's kind::i8 takes multiples of 32)
+  const int n_t = i8 ? (r + 31) / 32 * 32 : (r + 15) / 16 * 16;
   bool ok = pl.swap ? make_map(&maps.x, x, dtype, d_in, M, bn) : make_map(&maps.x, x, dtype, d_in, M, kBM);
   char* ws = static_cast<char*>(workspace);
   int tile0 = 0;
@@ -1578,6 +1720,8 @@ int run_dualpath(int n, const void* x, const void* const* W, const void* const* 
     GroupArgs& a = gp.g[g];
     a.ncols = d_out[g];
     a.scale = scale[g];
+    a.w_scale = i8 ? i8->w[g] : nullptr;
+    a.a_scale = i8 && adapter ? i8->a[g] : nullptr;
     a.y_ar = y_ar[g];
     a.y_draft = y_draft[g];
     a.stats_ar = stats_ar ? reinterpret_cast<float2*>(stats_ar[g]) : nullptr;
@@ -1593,8 +1737,8 @@ int run_dualpath(int n, const void* x, const void* const* W, const void* const* 
       a.tiles = a.tiles_a * ((M + bn - 1) / bn);
       ok = make_map(&maps.w[g], W[g], dtype, d_in, d_out[g], kBM);
       if (adapter)
-        ok = ok && make_map(&maps.bm[g], Bm[g], dtype, r, d_out[g], kBM) &&
-             make_map(&maps.t[g], a.t_buf, dtype, r, M, bn) &&
+        ok = ok && make_map(&maps.bm[g], Bm[g], t_dtype, r, d_out[g], kBM) &&
+             make_map(&maps.t[g], a.t_buf, t_dtype, r, M, bn) &&
              make_map(&maps.l[g], A[g], dtype, d_in, r, kBM);
     } else {
       // a CTA pair per 256 x 256 tile (each CTA: 128 rows of x, 128 rows of W);
@@ -1603,11 +1747,11 @@ int run_dualpath(int n, const void* x, const void* const* W, const void* const* 
       a.tiles = a.tiles_a * ((d_out[g] + 255) / 256);
       ok = make_map(&maps.w[g], W[g], dtype, d_in, d_out[g], kBM);
       if (adapter)
-        ok = ok && make_map(&maps.bm[g], Bm[g], dtype, r, d_out[g], kBM) &&
-             make_map(&maps.t[g], a.t_buf, dtype, r, M, kBM) &&
+        ok = ok && make_map(&maps.bm[g], Bm[g], t_dtype, r, d_out[g], kBM) &&
+             make_map(&maps.t[g], a.t_buf, t_dtype, r, M, kBM) &&
              make_map(&maps.l[g], A[g], dtype, d_in, r, n_t / 2);
       // output maps of the TMA-store epilogue (bf16): 32 rows x 64 columns
-      if (ok && adapter && dtype == UNO_BF16) {
+      if (ok && adapter && sizeof(Y) == 2 && d_out[g] % 8 == 0) {
         ok = make_store_map(&maps.yd[g], y_draft[g], d_out[g], M);
         if (ok && y_ar[g]) ok = make_store_map(&maps.ya[g], y_ar[g], d_out[g], M);
       }
@@ -1630,13 +1774,13 @@ int run_dualpath(int n, const void* x, const void* const* W, const void* const* 
       return UNO_ERR_CUDA;
   }
   if (pl.swap) {
-    gp.idesc_t = sm100::instr_desc(tf32, kBM, bn);
+    gp.idesc_t = i8 ? sm100::instr_desc_i8(kBM, bn) : sm100::instr_desc(tf32, kBM, bn);
     gp.t_brows = bn;
-    return launch_swapped<T>(bn, maps, gp, st);
+    return launch_swapped<T, Y>(bn, maps, gp, st);
   }
-  gp.idesc_t = sm100::instr_desc(tf32, 2 * kBM, n_t);
+  gp.idesc_t = i8 ? sm100::instr_desc_i8(2 * kBM, n_t) : sm100::instr_desc(tf32, 2 * kBM, n_t);
   gp.t_brows = n_t / 2;
-  return launch_dual<T, 256, false, true>(maps, gp, st);
+  return launch_dual<T, Y, 256, false, true>(maps, gp, st);
 }
 
 // Argument checks shared by the single and the grouped entry points.
@@ -1644,7 +1788,6 @@ int check_dual_args(int n, const void* x, const void* const* W, const void* cons
                     const void* const* Bm, void* const* y_ar, void* const* y_draft, int M,
                     int d_in, const int* d_out, int r, int dtype, const void* workspace,
                     size_t workspace_bytes) {
-  if (dtype != UNO_BF16 && dtype != UNO_F32) return UNO_ERR_DTYPE;
   if (n < 1 || n > kMaxGroups) return UNO_ERR_SIZE;
   if (!W || !y_ar || !y_draft || !d_out) return UNO_ERR_NULL;
   for (int g = 0; g < n; ++g)
@@ -1674,6 +1817,7 @@ int dispatch(int n, const void* x, const void* const* W, const void* const* A,
              void* const* y_draft, int M, int d_in, const int* d_out, int r, int dtype,
              void* workspace, size_t workspace_bytes, void* stream,
              float* const* stats_ar = nullptr, float* const* stats_draft = nullptr) {
+  if (dtype != UNO_BF16 && dtype != UNO_F32) return UNO_ERR_DTYPE;
   const int chk = check_dual_args(n, x, W, A, Bm, y_ar, y_draft, M, d_in, d_out, r, dtype,
                                   workspace, workspace_bytes);
   if (chk != 1) return chk;
@@ -1690,14 +1834,14 @@ int dispatch(int n, const void* x, const void* const* W, const void* const* A,
 }  // namespace
 
 extern "C" size_t uno_dualpath_workspace_bytes(int M, int d_in, int d_out, int r, int dtype) {
-  if (!dual_sizes_ok(M, d_in, d_out, r, dtype)) return 0;
+  if (dtype == kInt8 || !dual_sizes_ok(M, d_in, d_out, r, dtype)) return 0;
   const Plan pl = make_plan(M, d_in, r, dtype);
   return pl.t_bytes + pl.flag_bytes + pl.part_bytes;
 }
 
 extern "C" size_t uno_dualpath_grouped_workspace_bytes(int n, int M, int d_in, const int* d_out,
                                                        int r, int dtype) {
-  if (n < 1 || n > kMaxGroups || !d_out) return 0;
+  if (n < 1 || n > kMaxGroups || !d_out || dtype == kInt8) return 0;
   for (int g = 0; g < n; ++g)
     if (!dual_sizes_ok(M, d_in, d_out[g], r, dtype)) return 0;
   const Plan pl = make_plan(M, d_in, r, dtype);
@@ -1751,6 +1895,41 @@ extern "C" int uno_dualpath_linear_stats(const void* x, const void* W, const voi
   if (!uno_host::aligned(stats_ar, 8) || !uno_host::aligned(stats_draft, 8)) return UNO_ERR_ALIGN;
   return dispatch(1, x, &W, &A, &Bm, &scale, gate, &y_ar, &y_draft, M, d_in, &d_out, r, dtype,
                   workspace, workspace_bytes, stream, &stats_ar, &stats_draft);
+}
+
+extern "C" size_t uno_dualpath_int8_workspace_bytes(int M, int d_in, int d_out, int r) {
+  if (r == 0) r = 8;  // no adapter
+  if (!dual_sizes_ok(M, d_in, d_out, r, kInt8)) return 0;
+  const Plan pl = make_plan(M, d_in, r, kInt8);
+  return pl.t_bytes + pl.flag_bytes + pl.part_bytes;
+}
+
+extern "C" int uno_dualpath_linear_int8(const int8_t* x, const float* x_scale, const int8_t* W,
+                                        const float* w_scale, const int8_t* A,
+                                        const float* a_scale, const void* Bm, float scale,
+                                        const uint8_t* gate, void* y_ar, void* y_draft, int M,
+                                        int d_in, int d_out, int r, int out_dtype,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+  if (out_dtype != UNO_BF16 && out_dtype != UNO_F32) return UNO_ERR_DTYPE;
+  if (y_draft && r == 0) return UNO_ERR_SIZE;
+  if (r == 0) r = 8;  // AR weights alone: no adapter is read
+  const void *W0 = W, *A0 = A;
+  const int chk = check_dual_args(1, x, &W0, &A0, &Bm, &y_ar, &y_draft, M, d_in, &d_out, r, kInt8,
+                                  workspace, workspace_bytes);
+  if (chk != 1) return chk;
+  if (!x_scale || !w_scale || (y_draft && !a_scale)) return UNO_ERR_NULL;
+  for (const float* s : {x_scale, w_scale, a_scale})
+    if (!uno_host::aligned(s, 16)) return UNO_ERR_ALIGN;
+  const int dev = uno_host::check_device();
+  if (dev != UNO_OK) return dev;
+  const Int8Scales i8{x_scale, &w_scale, &a_scale};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (out_dtype == UNO_BF16)
+    return run_dualpath<int8_t, uint16_t>(1, x, &W0, &A0, &Bm, &scale, gate, &y_ar, &y_draft, M,
+                                          d_in, &d_out, r, kInt8, workspace, st, nullptr, nullptr,
+                                          &i8);
+  return run_dualpath<int8_t, float>(1, x, &W0, &A0, &Bm, &scale, gate, &y_ar, &y_draft, M, d_in,
+                                     &d_out, r, kInt8, workspace, st, nullptr, nullptr, &i8);
 }
 
 extern "C" int uno_dualpath_test_hooks(uint64_t wait_ns, uint32_t t_flag_skew) {

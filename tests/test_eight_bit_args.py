@@ -62,3 +62,33 @@ def test_kv_append_args(lib):
                 dict(table=ODD), dict(scale=ODD)):
         assert call(**bad) == "UNO_ERR_ALIGN", bad
     assert call(B=0, k=None) == call(T=0, n=0, k=None) == "UNO_OK"
+
+
+def test_dualpath_int8_args(lib):
+    def call(x=FAKE, xs=FAKE, W=FAKE, ws=FAKE, A=FAKE, as_=FAKE, Bm=FAKE, ya=FAKE, yd=FAKE, M=4,
+             d_in=64, d_out=40, r=16, dtype=0, work=FAKE, nbytes=1 << 30):
+        return _name(lib.uno_dualpath_linear_int8(x, xs, W, ws, A, as_, Bm, 2.0, None, ya, yd, M,
+                                                  d_in, d_out, r, dtype, work, nbytes, None))
+
+    assert call(dtype=2) == "UNO_ERR_DTYPE"
+    for bad in (dict(M=-1), dict(d_in=0), dict(d_in=40), dict(d_in=65552), dict(d_out=0),
+                dict(r=12), dict(r=264), dict(r=0), dict(r=-8)):
+        assert call(**bad) == "UNO_ERR_SIZE", bad
+    for bad in (dict(x=None), dict(xs=None), dict(W=None), dict(ws=None), dict(A=None),
+                dict(as_=None), dict(Bm=None), dict(ya=None, yd=None)):
+        assert call(**bad) == "UNO_ERR_NULL", bad
+    for bad in (dict(x=ODD), dict(xs=ODD), dict(W=ODD), dict(ws=ODD), dict(A=ODD), dict(as_=ODD),
+                dict(Bm=ODD), dict(ya=ODD), dict(yd=ODD), dict(work=ODD)):
+        assert call(**bad) == "UNO_ERR_ALIGN", bad
+    assert call(work=None) == call(nbytes=64) == "UNO_ERR_WORKSPACE"
+    assert call(M=0, x=None) == "UNO_OK"
+    assert lib.uno_dualpath_int8_workspace_bytes(17, 4096, 1000, 128) >= 17 * 128 * 2
+    assert lib.uno_dualpath_int8_workspace_bytes(17, 4096, 1000, 0) > 0
+    assert lib.uno_dualpath_int8_workspace_bytes(17, 4090, 1000, 0) == 0
+
+
+def test_the_operand_type_of_the_8_bit_call_is_no_dtype_of_the_others(lib):
+    for code in (2, 3, -1, -8):
+        assert lib.uno_dualpath_workspace_bytes(16, 64, 64, 8, code) == 0
+        assert _name(lib.uno_dualpath_linear(FAKE, FAKE, FAKE, FAKE, 2.0, FAKE, FAKE, 16, 64, 64,
+                                             8, code, FAKE, 1 << 30, None)) == "UNO_ERR_DTYPE"
