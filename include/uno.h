@@ -477,12 +477,55 @@ int uno_kv_append(const void* k_new, const void* v_new, const int32_t* start,
                   void* v_codes, float* k_scale, float* v_scale, void* stream);
 
 /* ------------------------------------------------------------------------ *
+ * Attention of a drafted block or tree over the paged 8-bit cache
+ *
+ * Verification runs the AR model over all positions of a block in one pass
+ * (reader page, "The Psi-Speculative Sampler"; every prefix of the tree in
+ * "Sampler Extensions"); its attention reads the sequence's cached tokens and
+ * the block's own. For new token i of sequence b and query head h (KV head
+ * h / (Hq / Hkv)):
+ *   out = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale q . k_j)
+ * over all cached positions j < lens[b] and the new tokens that i sees: j <= i,
+ * or with `parent` i itself and its chain of parents. T = 1 is plain decode.
+ * Float32 softmax and sums; cached values are code * scale as uno_kv_append
+ * writes them (any scales >= 0; value scales outside [2^-60, 2^60] count as the
+ * nearer of the two), new ones the bf16 rows.
+ *
+ * q, out       [B, T, Hq, D] bf16;  k_new, v_new [B, T, Hkv, D] bf16
+ * lens         [B] int32 cached tokens; one outside [0, width * page] makes the
+ *              sequence's rows NaN, as does a page id outside [0, num_pages)
+ *              among its pages
+ * parent       [B, T] int32 or NULL: node i's parent, before it (the node order
+ *              of uno_tree_draft); a value outside [0, i) ends the chain
+ * num_new      [B] int32 or NULL: rows i >= num_new[b] (clamped to [0, T]) are
+ *              neither read nor written (uno_tree_draft's n_nodes)
+ * scale        softmax scale, finite
+ * What a row does not see does not reach it: masked tokens and slots behind
+ * lens[b] may hold infinities and NaN.
+ * Limits: B <= 65535, T <= 4096, Hkv <= 1024, Hq <= 16384 a multiple of Hkv, D 64 or
+ * 128, page 16, 32, 64 or 128, width * page <= 2^30, num_pages * Hkv * page < 2^31.
+ * workspace    at least uno_block_attention_workspace_bytes(...) bytes, 16-byte
+ *              aligned, contents irrelevant on entry. Two calls that share one
+ *              must be ordered on one stream.
+ * Deterministic for a given device and call; how a sequence's sum is split
+ * depends on all lengths of the call, so its last bits can differ between batches.
+ * ------------------------------------------------------------------------ */
+size_t uno_block_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
+int uno_block_attention(const void* q, const void* k_new, const void* v_new, const int32_t* lens,
+                        const int32_t* parent, const int32_t* num_new, float scale, int B, int T,
+                        int Hq, int Hkv, int D, int page, const int32_t* page_table, int width,
+                        int num_pages, const void* k_codes, const void* v_codes,
+                        const float* k_scale, const float* v_scale, void* out, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ *
  * Device fault flags
  *
  * Every wait inside the kernels is bounded in time. A wait that gives up
  * (which correct code never does) sets a bit here, abandons its work and lets
  * the kernel exit instead of hanging the GPU: bit 0 TMA producer, bit 1 MMA
- * issuer, bit 2 epilogue. This call synchronises the device, writes the
+ * issuer, bit 2 epilogue of the dual-path linear, bit 3 TMA producer, bit 4
+ * consumer of the block attention. This call synchronises the device, writes the
  * current flags to *flags and clears them when `clear` is non-zero.
  * ------------------------------------------------------------------------ */
 int uno_device_fault_flags(int clear, unsigned int* flags);

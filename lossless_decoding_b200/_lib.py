@@ -98,6 +98,11 @@ def _load() -> ctypes.CDLL:
     L.uno_kv_append.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, i32, i32,
                                 vp, vp, vp, vp, vp]
     L.uno_kv_append.restype = i32
+    L.uno_block_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    L.uno_block_attention_workspace_bytes.restype = sz
+    L.uno_block_attention.argtypes = [vp, vp, vp, vp, vp, vp, ctypes.c_float, i32, i32, i32, i32,
+                                      i32, i32, vp, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.uno_block_attention.restype = i32
     L.uno_device_fault_flags.argtypes = [i32, ctypes.POINTER(ctypes.c_uint)]
     L.uno_device_fault_flags.restype = i32
     L.uno_dualpath_test_hooks.argtypes = [u64, ctypes.c_uint32]

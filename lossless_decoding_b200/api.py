@@ -753,6 +753,51 @@ def kv_append(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, start: t
         raise UnoError(st, "uno_kv_append")
 
 
+def block_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, cache: KvCache,
+                    lens: torch.Tensor, *, parent: Optional[torch.Tensor] = None,
+                    num_new: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                    out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of T new tokens per sequence over its cached tokens and each other.
+
+    q [B, T, Hq, D], k_new, v_new [B, T, Hkv, D] bfloat16; lens [B] int32 cached
+    tokens of each sequence. New token i sees new tokens j <= i, or with parent
+    [B, T] int32 (a tree's ``node_parent``) itself and its ancestors. num_new [B]
+    int32 (a tree's ``n_nodes``): later rows are not computed and keep what `out`
+    holds (zeros when `out` is allocated here). scale defaults to D ** -0.5. Returns out
+    [B, T, Hq, D]. The new tokens are not appended: see ``kv_append``.
+    """
+    if q.dim() != 4 or k_new.dim() != 4:
+        raise ValueError("q must be [B, T, Hq, D], k_new and v_new [B, T, Hkv, D]")
+    B, T, Hq, D = q.shape
+    Hkv = k_new.shape[2]
+    _expect("q", q, (B, T, Hq, D), torch.bfloat16)
+    _expect("k_new", k_new, (B, T, Hkv, D), torch.bfloat16)
+    _expect("v_new", v_new, (B, T, Hkv, D), torch.bfloat16)
+    _expect("lens", lens, (B,), torch.int32)
+    _expect("parent", parent, (B, T), torch.int32)
+    _expect("num_new", num_new, (B,), torch.int32)
+    _expect("out", out, (B, T, Hq, D), torch.bfloat16)
+    _check_cache(cache, B, Hkv, D)
+    dev = _check_cuda(q, k_new, v_new, lens, parent, num_new, out, cache.k, cache.v,
+                      cache.k_scale, cache.v_scale, cache.page_table, workspace)
+    with _on(dev):
+        if out is None:
+            out = torch.empty_like(q) if num_new is None else torch.zeros_like(q)
+        if workspace is None:  # one of its own per call, as for dualpath_linear_int8
+            need = int(lib.uno_block_attention_workspace_bytes(B, T, Hq, Hkv, D))
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        st = lib.uno_block_attention(
+            _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(lens), _ptr(parent), _ptr(num_new),
+            D ** -0.5 if scale is None else float(scale), B, T, Hq, Hkv, D, cache.k.shape[2],
+            _ptr(cache.page_table), cache.page_table.shape[1], cache.k.shape[0], _ptr(cache.k),
+            _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale), _ptr(out), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream_handle(dev))
+    if st != 0:
+        raise UnoError(st, "uno_block_attention")
+    return out
+
+
 def device_fault_flags(clear: bool = True) -> int:
     """Fault bits set by a kernel wait that gave up (0 = none). Synchronises."""
     flags = ctypes.c_uint(0)

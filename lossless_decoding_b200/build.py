@@ -21,7 +21,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libuno.so")
 
 SOURCES = ["status.cu", "verify.cu", "verify_noalloc.cu", "dualpath.cu", "draft_sample.cu",
-           "tree_sampler.cu", "row_quant.cu", "kv_append.cu"]
+           "tree_sampler.cu", "row_quant.cu", "kv_append.cu",
+           "block_attention.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          f"-I{INCLUDE}"]

@@ -1833,6 +1833,12 @@ int dispatch(int n, const void* x, const void* const* W, const void* const* A,
 
 }  // namespace
 
+namespace uno_host {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return get_encode(); }
+
+}  // namespace uno_host
+
 extern "C" size_t uno_dualpath_workspace_bytes(int M, int d_in, int d_out, int r, int dtype) {
   if (dtype == kInt8 || !dual_sizes_ok(M, d_in, d_out, r, dtype)) return 0;
   const Plan pl = make_plan(M, d_in, r, dtype);
@@ -1941,8 +1947,11 @@ extern "C" int uno_dualpath_test_hooks(uint64_t wait_ns, uint32_t t_flag_skew) {
 extern "C" int uno_device_fault_flags(int clear, unsigned int* flags) {
   if (!flags) return UNO_ERR_NULL;
   if (cudaDeviceSynchronize() != cudaSuccess) return UNO_ERR_CUDA;
-  if (cudaMemcpyFromSymbol(flags, g_fault_flags, sizeof(unsigned)) != cudaSuccess)
+  unsigned attention = 0;
+  if (cudaMemcpyFromSymbol(flags, g_fault_flags, sizeof(unsigned)) != cudaSuccess ||
+      uno_host::attention_fault_flags(clear != 0, &attention) != UNO_OK)
     return UNO_ERR_CUDA;
+  *flags |= attention;
   if (clear) {
     const unsigned zero = 0;
     if (cudaMemcpyToSymbol(g_fault_flags, &zero, sizeof(unsigned)) != cudaSuccess)

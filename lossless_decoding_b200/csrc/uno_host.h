@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include "uno.h"
@@ -16,6 +17,13 @@ inline bool aligned(const void* p, uintptr_t a) {
 // UNO_ERR_DEVICE otherwise, UNO_ERR_CUDA when the runtime cannot say. The
 // answer is cached per device ordinal.
 int check_device();
+
+// cuTensorMapEncodeTiled (dualpath.cu), or null when the driver lacks it.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+// Fault bits of the block attention's waits (block_attention.cu); the caller
+// has synchronised the device.
+int attention_fault_flags(bool clear, unsigned* flags);
 
 // One inverse-CDF draw per softmax row (draft_sample.cu): row n of sequence b
 // (logits + ((b * rows_per_seq + n) * V)) draws with the uniform of Philox

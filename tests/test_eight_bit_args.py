@@ -92,3 +92,28 @@ def test_the_operand_type_of_the_8_bit_call_is_no_dtype_of_the_others(lib):
         assert lib.uno_dualpath_workspace_bytes(16, 64, 64, 8, code) == 0
         assert _name(lib.uno_dualpath_linear(FAKE, FAKE, FAKE, FAKE, 2.0, FAKE, FAKE, 16, 64, 64,
                                              8, code, FAKE, 1 << 30, None)) == "UNO_ERR_DTYPE"
+
+
+def test_block_attention_args(lib):
+    def call(q=FAKE, k=FAKE, lens=FAKE, parent=None, nn=None, scale=0.1, B=2, T=4, Hq=4, H=2, D=64,
+             page=16, table=FAKE, width=3, N=6, codes=FAKE, ks=FAKE, out=FAKE, work=FAKE,
+             nbytes=1 << 30):
+        return _name(lib.uno_block_attention(q, k, FAKE, lens, parent, nn, scale, B, T, Hq, H, D,
+                                             page, table, width, N, codes, FAKE, ks, FAKE, out,
+                                             work, nbytes, None))
+
+    for bad in (dict(B=-1), dict(B=65536), dict(T=-1), dict(T=4097), dict(Hq=3), dict(Hq=1),
+                dict(H=0), dict(Hq=16386, H=2), dict(D=80), dict(page=24), dict(width=-1),
+                dict(N=-1), dict(N=1 << 27), dict(scale=float("nan")), dict(scale=float("inf"))):
+        assert call(**bad) == "UNO_ERR_SIZE", bad
+    for bad in (dict(q=None), dict(k=None), dict(lens=None), dict(table=None), dict(codes=None),
+                dict(ks=None), dict(out=None)):
+        assert call(**bad) == "UNO_ERR_NULL", bad
+    for bad in (dict(q=ODD), dict(k=ODD), dict(lens=ODD), dict(parent=ODD), dict(nn=ODD),
+                dict(table=ODD), dict(codes=ODD), dict(ks=ODD), dict(out=ODD), dict(work=ODD)):
+        assert call(**bad) == "UNO_ERR_ALIGN", bad
+    assert call(work=None) == call(nbytes=64) == "UNO_ERR_WORKSPACE"
+    assert call(B=0, q=None) == call(T=0, q=None) == "UNO_OK"
+    assert lib.uno_block_attention_workspace_bytes(64, 17, 32, 8, 128) > 0
+    assert lib.uno_block_attention_workspace_bytes(64, 17, 33, 8, 128) == 0
+    assert lib.uno_block_attention_workspace_bytes(64, 17, 32, 8, 96) == 0
