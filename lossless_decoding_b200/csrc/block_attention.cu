@@ -6,36 +6,42 @@
 // of a block, or i's ancestors of a tree. Cached keys and values are e4m3 codes
 // with a scale per page and head; the new ones are bfloat16.
 //
-// Bound. A cached token costs 2 D bytes per KV head and 4 D flops per query row
-// (rows = new tokens x query heads per KV head). With few rows the stream of
-// codes bounds the call (HBM), past some 60 rows the products do.
+// Two launches. cached_kernel leaves float32 partial sums over the cached tokens
+// in the workspace, finish_kernel adds the new tokens and joins the partials.
 //
-// Split. The work items are (sequence, KV head, tile of query rows), each a list
-// of 64-token tiles of the cache and one unit for the new tokens. The units of
-// all items form one line that the CTAs share out evenly, whatever the lengths
-// of the sequences: a CTA's part starts and ends inside items, at most two of
-// its items are shared with other CTAs, and those leave their partial sums in
-// the workspace for the combine launch. (Lengths are on the device, so a split
+// Bound. A cached token costs 2 D bytes per KV head and 4 D flops per query row
+// (rows = new tokens x query heads per KV head): the stream of codes (HBM)
+// bounds the call as long as products and exponentials of a 128-token tile
+// stay under the 1420 clocks in which an SM's share of the bandwidth brings it.
+//
+// Split. The work items are (sequence, KV head, tile of 128 query rows), each a
+// list of 128-token tiles of the cache. The tiles of all items form one line
+// that the CTAs share out evenly, whatever the lengths of the sequences, so a
+// CTA's part starts and ends inside items. (Lengths are on the device: a split
 // planned on the host would have to assume the longest.)
 //
-// Arithmetic. mma.sync m16n8k16 with float32 accumulation. Codes are decoded to
-// half precision in registers (exact: e4m3 is a subset), queries are scaled per
-// row by a power of two into its range (bfloat16's 8 bits fit its 11). The value
-// scales go into the exponent: t = score log2(e) + log2(v_scale), the running
-// maximum is taken over t, and p = 2^(t - max) is at most 1 and rounded to half
-// (2^-11); the normaliser sums p / v_scale in float32. New tokens use bfloat16
-// products on the raw rows (p rounded to 2^-9).
+// Products. tcgen05, rows on the 128 TMEM lanes. Scores: kind::f8f6f4 on the codes
+// as they are; the queries are split into two e4m3 parts, q 2^s = hi + lo
+// (bfloat16's 8 bits are two signed 4-bit halves; 2^s brings the row's largest
+// into [128, 256), and what e4m3's smallest step 2^-9 drops is below 2^-18 of it).
+// Weighted values: kind::f16, weights rounded to half (2^-11) as the A operand in
+// TMEM over the scores they came from, values decoded to half in shared memory by
+// warps of their own (exact: e4m3 is a subset). With weights in e4m3 parts
+// the decode would go, but splitting a weight costs the softmax warps more than
+// the decode costs (7 clocks an element against 1).
 //
-// Layout. One thread's fragment of a contraction needs no particular order of
-// the contracted index, so the index is permuted until a thread's share is
-// contiguous: lane (g, c) (g = lane / 4, c = lane % 4) reads key bytes
-// [c D/4, (c + 1) D/4) of token g, and for values the D/8 bytes from g D/8
-// of the four tokens whose weights it already holds from the score
-// fragment. So codes go from TMA's swizzled tiles to registers in 16-byte
-// loads without bank conflicts and without a transpose.
+// Softmax. A row is a thread. Value scales go into the exponent: t = score
+// log2(e) + log2(v_scale), p = 2^(t - ref), and the normaliser sums p / v_scale in
+// float32. ref moves only when a tile's largest t exceeds it by 8 (then o and l
+// are rescaled and the tile's weights taken again), so the common tile is one
+// pass over the scores. With at most 64 (32) rows the lanes hold 2 (4) copies of
+// them, and each copy takes its half (quarter) of a tile's tokens: a warp's work
+// per tile falls with the rows, and the copies' sums are joined like those of
+// CTAs.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -48,15 +54,29 @@
 
 namespace {
 
-constexpr int kTile = 64;      // cached tokens per unit
-constexpr int kStages = 5;     // tiles in shared memory
+constexpr int kTile = 128;     // cached tokens per unit of work
+constexpr int kRows = 128;     // rows (TMEM lanes) of a tile
+constexpr int kStages = 4;     // tiles of codes in shared memory
 constexpr int kProducers = 2;  // TMA warps, alternating tiles
-constexpr int kMaxCtas = 2 * 148;
-constexpr uint64_t kWaitNs = 1000000000ull;
+// Warps: 0-3 softmax (TMEM lane quarter = warp), 4-7 value decode, then the
+// producers, then the MMA issuer (which owns TMEM).
+constexpr int kFirstProducer = 8;
+constexpr int kMmaWarp = kFirstProducer + kProducers;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kMaxCtas = 148;  // one CTA per SM
+constexpr long long kWaitClocks = 2000000000ll;  // bound of every wait: about a second
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLift = 8.f;   // log2 of how far a weight may pass 1 before its row's ref moves
+// Floor of a row's ref: a tile without a finite score leaves it there.
+constexpr float kLowest = -3.0e38f;
 
-enum : unsigned { kFaultProducer = 8u, kFaultConsumer = 16u };
+enum : unsigned { kFaultProducer = 8u, kFaultMma = 16u, kFaultSoftmax = 32u };
 __device__ unsigned int g_attn_fault;
+
+struct Head {
+  long long units;  // tiles of all items
+  int ctas;         // CTAs that have a part
+};
 
 struct AttnArgs {
   const uint16_t* q;      // [B][T][Hq][D]
@@ -70,22 +90,17 @@ struct AttnArgs {
   const int32_t* parent;  // [B][T] or null
   const int32_t* num_new; // [B] or null
   int B, T, Hq, Hkv, G, page, width, num_pages;
+  int copies;             // of the rows on the lanes: 4, 2 or 1
   float scale;            // softmax scale
-  struct Head* head;      // workspace
-  struct Desc* desc;      // [grid]
-  float2* part_ml;        // [grid][2][ROWS] running maximum and normaliser
-  float* part_o;          // [grid][2][ROWS][D]
-};
-
-struct Head {
-  long long units;
-  int ctas;  // CTAs that have a part
-};
-
-// The item that a CTA's part starts in.
-struct Desc {
-  long long start, end;  // its units
-  int b, h, rt, pad;
+  // workspace
+  Head* head;
+  long long* base;        // [B] first unit of each sequence
+  // partial sums of parts that begin an item: [B][Hkv][copies][T G], and of those
+  // that begin inside one (a CTA's first): [CTA][128 lanes]
+  float2* item_ml;        // (ref, normaliser)
+  float* item_o;          // [..][D]
+  float2* cta_ml;
+  float* cta_o;
 };
 
 // A sequence's share of the line of units.
@@ -98,25 +113,20 @@ struct Seq {
   long long units;
 };
 
-template <int ROWS>
 __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
   Seq s;
   s.len = a.lens[b];
   s.bad = s.len < 0 || s.len > a.width * a.page;
   if (s.bad) s.len = 0;
   s.nn = a.num_new ? min(max(a.num_new[b], 0), a.T) : a.T;
-  s.tiles = (s.len + kTile - 1) / kTile + 1;
-  s.rts = (s.nn * a.G + ROWS - 1) / ROWS;
+  s.tiles = (s.len + kTile - 1) / kTile;
+  s.rts = (s.nn * a.G + kRows - 1) / kRows;
   s.units = static_cast<long long>(a.Hkv) * s.rts * s.tiles;
   return s;
 }
 
-__device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ long long first_unit(const Head& h, int cta) {
+  return h.units * cta / h.ctas;
 }
 
 __device__ __forceinline__ void mma_bf16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -153,37 +163,127 @@ __device__ __forceinline__ bool nonfinite2(uint32_t w) {  // either bfloat16 of 
   return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
 }
 
-// Shared-memory plan of a variant.
-template <int D, int RW, int KW>
+
+__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float2 floats(uint32_t halves2) {
+  float2 f;
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(halves2));
+  return f;
+}
+
+// One thread waits for the phase with the given parity, giving up after about a
+// second (false then).
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity) {
+  if (sm100::mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t it = 1;; ++it) {
+    if (sm100::mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0 && clock64() - t0 > kWaitClocks) return false;
+  }
+}
+
+// The whole warp waits (one lane polls).
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = wait_one(bar, parity);
+  __syncwarp();
+  return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+}
+
+// D[tmem] (+)= A[tmem] B[smem desc], one thread. kF8: kind::f8f6f4, else kind::f16.
+template <bool kF8>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc,
+                                       bool accumulate) {
+  if constexpr (kF8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+}
+
+// Shared-memory descriptors. Codes of a tile of keys: K-major rows of D bytes (one
+// row per token), swizzled by TMA over the row's bytes (128 or 64), 8-row groups
+// 8 D bytes apart. Decoded values: MN-major, D on the MN side in atoms of 64
+// halves (128-byte rows, one per token, 128-byte swizzle): groups of 8 tokens
+// 1024 bytes apart (stride offset), the second 64 columns behind the tile's
+// tokens (leading offset).
+template <int D>
+__device__ __forceinline__ uint64_t key_desc(uint32_t saddr) {
+  uint64_t d = (saddr >> 4) & 0x3FFFu;
+  d |= static_cast<uint64_t>(1u) << 16;
+  d |= static_cast<uint64_t>((8 * D) >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(D == 128 ? 2u : 4u) << 61;
+  return d;
+}
+__device__ __forceinline__ uint64_t value_desc(uint32_t saddr) {
+  uint64_t d = (saddr >> 4) & 0x3FFFu;
+  d |= static_cast<uint64_t>((kTile * 128) >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// Shared memory: [stage]{keys, values}, two tiles of decoded values, scales
+// [stage][16-token group], barriers.
+template <int D>
 struct Plan {
-  static constexpr int kRows = 16 * RW;
-  static constexpr int kConsumers = RW * KW;
-  static constexpr int kThreads = 32 * (kConsumers + kProducers);
-  static constexpr int kStage = 2 * kTile * D;  // keys, values
-  static constexpr int kScales = kStages * kStage;               // float4 [stage][4 groups]
-  static constexpr int kMerge = kScales + kStages * 64;          // (KW - 1) warps' O, then m and l
-  static constexpr int kMergeWarp = 16 * D * 4 + 32 * 16;
-  static constexpr int kBars = kMerge + (KW - 1) * RW * kMergeWarp;
-  static constexpr int kBytes = kBars + 2 * kStages * 8 + 1024;  // + alignment
-  static constexpr int kCtasPerSm = kConsumers <= 4 ? 2 : 1;
+  static constexpr int kStage = 2 * kTile * D;
+  static constexpr int kHalfTile = kTile * D * 2;
+  static constexpr int kDecoded = kStages * kStage;
+  static constexpr int kScales = kDecoded + 2 * kHalfTile;
+  static constexpr int kBars = kScales + kStages * (kTile / 16) * 16;
+  static constexpr int kBytes = kBars + (2 * kStages + 9) * 8 + 8 + 1024;  // + alignment
+  static_assert(kBytes <= 232448, "dynamic shared memory per CTA (227 KB)");
 };
 
-template <int D, int RW, int KW>
-__global__ void __launch_bounds__(Plan<D, RW, KW>::kThreads, Plan<D, RW, KW>::kCtasPerSm)
-    attn_kernel(const __grid_constant__ CUtensorMap map_k,
-                const __grid_constant__ CUtensorMap map_v, const AttnArgs a) {
-  using P = Plan<D, RW, KW>;
-  constexpr int ROWS = P::kRows;
-  constexpr int KS = D / 16;       // k-steps of a score, 4 contiguous codes of a thread each
-  constexpr int DN = D / 8;        // output column tiles
-  constexpr int NT = 8 / KW;       // token n-tiles per warp and tile
-  constexpr int NG = NT / 2;       // groups of 16 tokens per warp and tile
+template <int D, int COPIES>
+__global__ void __launch_bounds__(kThreads, 1)
+    cached_kernel(const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v, const AttnArgs a) {
+  using P = Plan<D>;
+  constexpr int CW = kTile / COPIES;  // a softmax thread's tokens per tile
+  // TMEM columns: two score tiles (their weights over them), o, the queries' parts
+  constexpr uint32_t kColO = 2 * kTile, kColQ = kColO + D;
+  constexpr uint32_t kIdescS = (1u << 4) | ((kTile >> 3) << 17) | ((kRows >> 4) << 24);
+  constexpr uint32_t kIdescO =
+      (1u << 4) | (1u << 16) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((kRows >> 4) << 24);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   float4* s_scale = reinterpret_cast<float4*>(smem + P::kScales);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + P::kBars);
-  uint64_t* empty = full + kStages;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + P::kBars);  // codes and scales are there
+  uint64_t* empty = full + kStages;   // nobody needs them any more
+  uint64_t* s_full = empty + kStages; // [2] scores of a tile
+  uint64_t* p_full = s_full + 2;      // [2] weights of a tile
+  uint64_t* v_full = p_full + 2;      // [2] decoded values of a tile
+  uint64_t* o_done = v_full + 2;      // [2] a tile's weighted values are in o
+  uint64_t* q_full = o_done + 2;      // [1] a segment's queries
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(q_full + 1);
+  __shared__ uint64_t s_end;          // every MMA has completed
   __shared__ long long s_u0, s_u1, s_base;
   __shared__ int s_b;
   __shared__ volatile int s_abort;
@@ -192,19 +292,29 @@ __global__ void __launch_bounds__(Plan<D, RW, KW>::kThreads, Plan<D, RW, KW>::kC
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       sm100::mbar_init(&full[s], 1);
-      sm100::mbar_init(&empty[s], P::kConsumers);
+      sm100::mbar_init(&empty[s], 9);  // softmax and decode warps, the issuer's commit
     }
+    for (int k = 0; k < 2; ++k) {
+      sm100::mbar_init(&s_full[k], 1);
+      sm100::mbar_init(&p_full[k], 4);
+      sm100::mbar_init(&v_full[k], 4);
+      sm100::mbar_init(&o_done[k], 1);
+    }
+    sm100::mbar_init(q_full, 4);
+    sm100::mbar_init(&s_end, 1);
     s_abort = 0;
     sm100::fence_mbar_init();
   }
-  uno::launch_dependents();
+  if (warp == kMmaWarp) sm100::tmem_alloc(tmem_holder, 512);
   uno::grid_dependency_wait();
+  // finish_kernel may start: what it reads before its own wait is older than this launch
+  uno::launch_dependents();
 
   // This CTA's part [u0, u1) of the line, and the sequence it starts in.
   if (warp == 0) {
     long long total = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-      long long n = b0 + lane < a.B ? seq_of<ROWS>(a, b0 + lane).units : 0;
+      long long n = b0 + lane < a.B ? seq_of(a, b0 + lane).units : 0;
 #pragma unroll
       for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
       total += n;
@@ -213,23 +323,25 @@ __global__ void __launch_bounds__(Plan<D, RW, KW>::kThreads, Plan<D, RW, KW>::kC
     const int i = blockIdx.x;
     const long long u0 = i < ctas ? total * i / ctas : total;
     const long long u1 = i < ctas ? total * (i + 1) / ctas : total;
-    long long base = 0;
+    long long base = 0, my_base = 0;
     int at = 0;
-    if (u0 < u1) {
-      for (int b0 = 0;; b0 += 32) {  // ends: u0 < total
-        const long long n = b0 + lane < a.B ? seq_of<ROWS>(a, b0 + lane).units : 0;
+    if (u0 < u1 || i == 0) {
+      bool found = u0 >= u1;
+      for (int b0 = 0; b0 < a.B && !(found && i != 0); b0 += 32) {
+        const long long n = b0 + lane < a.B ? seq_of(a, b0 + lane).units : 0;
         long long pre = n;  // inclusive prefix over the lanes
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const long long up = __shfl_up_sync(0xFFFFFFFFu, pre, o);
           if (lane >= o) pre += up;
         }
+        if (i == 0 && b0 + lane < a.B) a.base[b0 + lane] = base + pre - n;
         const unsigned in = __ballot_sync(0xFFFFFFFFu, u0 < base + pre);
-        if (in) {
+        if (in && !found) {
           const int l = __ffs(in) - 1;
-          base += __shfl_sync(0xFFFFFFFFu, pre - n, l);
+          my_base = base + __shfl_sync(0xFFFFFFFFu, pre - n, l);
           at = b0 + l;
-          break;
+          found = true;
         }
         base += __shfl_sync(0xFFFFFFFFu, pre, 31);
       }
@@ -237,28 +349,31 @@ __global__ void __launch_bounds__(Plan<D, RW, KW>::kThreads, Plan<D, RW, KW>::kC
     if (lane == 0) {
       s_u0 = u0;
       s_u1 = u1;
-      s_base = base;
+      s_base = my_base;
       s_b = at;
       if (i == 0) *a.head = Head{total, ctas};
     }
   }
+  sm100::tc_fence_before();
   __syncthreads();
+  sm100::tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
   const long long u0 = s_u0, u1 = s_u1;
 
   // A segment: the part of one item that this CTA does.
   struct Segment {
     Seq s;
-    int b, h, rt, t0, t1;  // units [t0, t1) of the item
+    int b, h, rt, t0, t1;  // tiles [t0, t1) of the item
     long long start;       // the item's first unit
   };
   long long base = s_base;
   int b = s_b;
   auto segment_at = [&](long long u) {
     Segment g;
-    g.s = seq_of<ROWS>(a, b);
+    g.s = seq_of(a, b);
     while (u >= base + g.s.units) {
       base += g.s.units;
-      g.s = seq_of<ROWS>(a, ++b);
+      g.s = seq_of(a, ++b);
     }
     g.b = b;
     const int item = static_cast<int>((u - base) / g.s.tiles);
@@ -269,10 +384,70 @@ __global__ void __launch_bounds__(Plan<D, RW, KW>::kThreads, Plan<D, RW, KW>::kC
     g.rt = item - g.h * g.s.rts;
     return g;
   };
+  auto give_up = [&](unsigned bit) {
+    if (lane == 0) atomicOr(&g_attn_fault, bit);
+    s_abort = 1;
+  };
 
-  if (warp >= P::kConsumers) {
+  if (warp == kMmaWarp) {
+    // ---- MMA issuer ----
+    if (lane == 0) {
+      bool ok = true;
+      auto need = [&](uint64_t* bar, uint32_t parity) {
+        if (ok && (s_abort || !wait_one(bar, parity))) {
+          give_up(kFaultMma);
+          ok = false;
+        }
+        return ok;
+      };
+      auto scores = [&](int it) {
+        const int s = it % kStages;
+        if (!need(&full[s], (it / kStages) & 1)) return;
+        sm100::tc_fence_after();
+        const uint64_t kd = key_desc<D>(sm100::smem_addr(smem + s * P::kStage));
+        const uint32_t d = tmem + (it & 1) * kTile;
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)  // 32 codes: 32 bytes, 8 columns of queries
+            mma_ts<true>(d, tmem + kColQ + part * (D / 4) + 8 * k, kd + 2 * k, kIdescS,
+                         part + k > 0);
+        sm100::mma_commit(&s_full[it & 1]);
+        sm100::mma_commit(&empty[s]);
+      };
+      auto values = [&](int it, bool first) {
+        const int k2 = it & 1;
+        if (!need(&p_full[k2], (it >> 1) & 1) || !need(&v_full[k2], (it >> 1) & 1)) return;
+        sm100::tc_fence_after();
+        const uint64_t vd =
+            value_desc(sm100::smem_addr(smem + P::kDecoded + k2 * P::kHalfTile));
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)  // 16 tokens: 8 columns of weights, 2048 bytes
+          mma_ts<false>(tmem + kColO, tmem + k2 * kTile + 8 * k, vd + k * 128, kIdescO,
+                        !first || k > 0);
+        sm100::mma_commit(&o_done[k2]);
+      };
+      int it = 0, seg = 0;
+      for (long long u = u0; u < u1 && ok; ++seg) {
+        const Segment g = segment_at(u);
+        const int n = g.t1 - g.t0;
+        // the segment's queries are stored only after its predecessor's o was read
+        if (!need(q_full, seg & 1)) break;
+        sm100::tc_fence_after();
+        scores(it);
+        for (int j = 0; j < n && ok; ++j) {
+          if (j + 1 < n) scores(it + j + 1);  // ahead of this tile's softmax
+          if (ok) values(it + j, j == 0);
+        }
+        it += n;
+        u = g.start + g.t1;
+      }
+      sm100::mma_commit(&s_end);
+      if (!wait_one(&s_end, 0)) give_up(kFaultMma);
+    }
+  } else if (warp >= kFirstProducer) {
     // ---- producers: tiles of the cache, alternating ----
-    const int pr = warp - P::kConsumers;
+    const int pr = warp - kFirstProducer;
     const int unit = min(a.page, kTile);  // tokens per TMA copy
     const int per = kTile / unit;         // copies per tile (and of keys and values each)
     int it = 0;                           // tiles of this CTA so far, over all segments
@@ -280,8 +455,7 @@ __global__ void __launch_bounds__(Plan<D, RW, KW>::kThreads, Plan<D, RW, KW>::kC
     bool ok = true;
     for (long long u = u0; u < u1 && ok;) {
       const Segment g = segment_at(u);
-      const int end = min(g.t1, g.s.tiles - 1);  // the last unit is the new tokens
-      const int n = max(end - g.t0, 0);
+      const int n = g.t1 - g.t0;
       // 32 / per of this warp's tiles at a time: page ids and scales of all their
       // copies in one round of loads, a copy per lane
       const int batch = 32 / per;
@@ -298,25 +472,20 @@ __global__ void __launch_bounds__(Plan<D, RW, KW>::kThreads, Plan<D, RW, KW>::kC
         const float ks = have ? a.k_scale[at] : wanted ? __uint_as_float(0x7FC00000u) : 0.f;
         const float vs = have ? a.v_scale[at] : 1.f;
         const float vc = fminf(fmaxf(vs, 8.67361738e-19f), 1.15292150e18f);  // 2^-60 .. 2^60
-        const float lv = vs != vs ? vs : log2f(vc);
+        const float4 sc = make_float4(ks, vs != vs ? vs : log2f(vc), 1.f / vc, 0.f);
         const int row = static_cast<int>(at) * a.page + pos % a.page;
         for (int k = 0; k < batch && j0 + k * kProducers < n; ++k) {
           const int i = it + j0 + k * kProducers;
           const int s = i % kStages;
-          bool bad = i >= kStages && !sm100::mbar_wait(&empty[s], ((i / kStages) - 1) & 1, kWaitNs);
-          if (bad) {
-            atomicOr(&g_attn_fault, kFaultProducer);
-            s_abort = 1;
-          }
-          if (__any_sync(0xFFFFFFFFu, bad || s_abort)) {
+          if (i >= kStages && !wait(&empty[s], ((i / kStages) - 1) & 1)) give_up(kFaultProducer);
+          if (__any_sync(0xFFFFFFFFu, s_abort)) {
             ok = false;
             break;
           }
           const bool turn = lane / per == k;
           if (turn) {
             const int first = lane % per * (unit / 16);
-            for (int e = 0; e < unit / 16; ++e)
-              s_scale[s * 4 + first + e] = make_float4(ks, lv, 1.f / vc, 0.f);
+            for (int e = 0; e < unit / 16; ++e) s_scale[s * (kTile / 16) + first + e] = sc;
           }
           const int copies = __popc(__ballot_sync(0xFFFFFFFFu, turn && have));
           __syncwarp();
@@ -335,488 +504,608 @@ __global__ void __launch_bounds__(Plan<D, RW, KW>::kThreads, Plan<D, RW, KW>::kC
       u = g.start + g.t1;
     }
     // No copy may still be landing when the CTA exits: wait for this warp's
-    // among the last kStages tiles (the consumers have done so too, unless
-    // they have given up).
+    // among the last kStages tiles (their readers have done so too, unless they
+    // have given up).
     for (int i = max((ok ? it : mine + 1) - kStages, 0); i <= mine; ++i)
-      if (i % kProducers == pr) sm100::mbar_wait(&full[i % kStages], (i / kStages) & 1, kWaitNs);
-  } else {
-    // ---- consumers: warp (rw, kw) has rows 16 rw.. and every KW-th share of a tile's tokens ----
-    const int rw = warp % RW, kw = warp / RW;
-    const int g = lane >> 2, c = lane & 3;
-    bool ok = true;
+      if (i % kProducers == pr) wait(&full[i % kStages], (i / kStages) & 1);
+  } else if (warp >= 4) {
+    // ---- value decode: codes of a tile to halves ----
+    const int tid = threadIdx.x - 128;
     int it = 0;
-    for (long long u = u0; u < u1;) {
-      const Segment sg = segment_at(u);
-      const int R = sg.s.nn * a.G;           // rows of the sequence and head
-      const int r0 = sg.rt * ROWS + rw * 16; // this warp's first row
-      const int rows[2] = {r0 + g, r0 + g + 8};
-      // query row r: token r / G, head h * G + r % G
-      size_t q_at[2];
-      int tok[2];
-      uint32_t qa[KS][4];
-      float qf[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = min(rows[i], R - 1);  // rows past the end repeat the last one, unstored
-        tok[i] = r / a.G;
-        q_at[i] = ((static_cast<size_t>(sg.b) * a.T + tok[i]) * a.Hq + sg.h * a.G + r % a.G) * D;
-      }
-      const bool live = r0 < R;  // warp-uniform
-      auto load_q = [&](int i, uint32_t* w) {
-        const uint4* p = reinterpret_cast<const uint4*>(a.q + q_at[i] + c * (D / 4));
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          const uint4 v = __ldg(p + k);
-          w[4 * k] = v.x;
-          w[4 * k + 1] = v.y;
-          w[4 * k + 2] = v.z;
-          w[4 * k + 3] = v.w;
+    bool ok = true;
+    for (long long u = u0; u < u1 && ok;) {
+      const Segment g = segment_at(u);
+      for (int ti = g.t0; ti < g.t1; ++ti, ++it) {
+        const int s = it % kStages, k2 = it & 1;
+        if (!wait(&full[s], (it / kStages) & 1) ||
+            (it >= 2 && !wait(&o_done[k2], ((it >> 1) - 1) & 1))) {
+          give_up(kFaultSoftmax);
+          ok = false;
+          break;
         }
-      };
+        const uint8_t* src = smem + s * P::kStage + kTile * D;
+        uint8_t* dst = smem + P::kDecoded + k2 * P::kHalfTile;
+        const int left = g.s.len - ti * kTile;
+        constexpr int kPieces = D / 16;  // 16-byte pieces of a token
+        const int ch = tid % kPieces;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t w[D / 8];
-        load_q(i, w);
-        uint32_t top = 0;
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        // the row's largest magnitude moves to [2^13, 2^14)
-        const int sh = min(13 + 127 - static_cast<int>(top >> 7), 120);
-        const float f = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
-        qf[i] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          qa[k][i] = pack_f16(bf_lo(w[2 * k]) * f, bf_hi(w[2 * k]) * f);
-          qa[k][i + 2] = pack_f16(bf_lo(w[2 * k + 1]) * f, bf_hi(w[2 * k + 1]) * f);
+        for (int st = 0; st < kTile * kPieces / 128; ++st) {
+          const int t = tid / kPieces + st * (128 / kPieces);
+          const int sw = D == 128 ? (t & 7) : ((t >> 1) & 3);
+          uint4 w = *reinterpret_cast<const uint4*>(src + t * D + ((ch ^ sw) << 4));
+          // slots behind the sequence may hold anything, NaN too
+          if (t >= left) w = make_uint4(0u, 0u, 0u, 0u);
+          const uint4 x = make_uint4(halves(w.x & 0xFFFFu), halves(w.x >> 16),
+                                     halves(w.y & 0xFFFFu), halves(w.y >> 16));
+          const uint4 y = make_uint4(halves(w.z & 0xFFFFu), halves(w.z >> 16),
+                                     halves(w.w & 0xFFFFu), halves(w.w >> 16));
+          // columns 16 ch.. : chunks 2 (ch % 4), + 1 of the token's row in its half
+          uint8_t* row = dst + (ch >> 2) * (kTile * 128) + t * 128;
+          const int c0 = (ch & 3) * 2, r = t & 7;
+          const int flip = (ch >> 2) & 1;  // lanes of the two halves write different banks
+          *reinterpret_cast<uint4*>(row + (((c0 + flip) ^ r) << 4)) = flip ? y : x;
+          *reinterpret_cast<uint4*>(row + (((c0 + 1 - flip) ^ r) << 4)) = flip ? x : y;
         }
-      }
-      float o[DN][4];
-#pragma unroll
-      for (int i = 0; i < DN; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-      // New reference for t[n][..] (n n-tiles): weights in place, o and l rescaled.
-      auto rescale = [&](float (*t)[4], int n) {
-        float mx[2] = {m[0], m[1]};
-        for (int j = 0; j < n; ++j) {
-          mx[0] = fmaxf(mx[0], fmaxf(t[j][0], t[j][1]));
-          mx[1] = fmaxf(mx[1], fmaxf(t[j][2], t[j][3]));
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 1));
-          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 2));
-        }
-        const bool up = mx[0] > m[0] || mx[1] > m[1];
-        if (__any_sync(0xFFFFFFFFu, up)) {
-          float al[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            al[i] = m[i] == -INFINITY ? 0.f : uno::ex2(m[i] - mx[i]);
-            l[i] *= al[i];
-            m[i] = mx[i];
-          }
-#pragma unroll
-          for (int j = 0; j < DN; ++j) {
-            o[j][0] *= al[0];
-            o[j][1] *= al[0];
-            o[j][2] *= al[1];
-            o[j][3] *= al[1];
-          }
-        }
-        const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-        for (int j = 0; j < n; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) t[j][e] = uno::ex2(t[j][e] - ref[e >> 1]);
-      };
-
-      // ---- cached tokens ----
-      const int end = min(sg.t1, sg.s.tiles - 1);
-      for (int ti = sg.t0; ti < end; ++ti, ++it) {
-        const int s = it % kStages;
-        if (ok && !sm100::mbar_wait(&full[s], (it / kStages) & 1, kWaitNs)) {
-          if (lane == 0) atomicOr(&g_attn_fault, kFaultConsumer);
-          s_abort = 1;
-          ok = false;  // go on without waiting: the results are abandoned
-        }
-        if (live) {
-          const uint8_t* sk = smem + s * P::kStage;
-          const uint8_t* sv = sk + kTile * D;
-          const int left = sg.s.len - ti * kTile;  // tokens of the tile that exist
-          float t[NT][4];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const int tr = (kw * NT + n) * 8 + g;
-            uint32_t w[D / 16];
-            if constexpr (D == 128) {
-              const uint4 x = *reinterpret_cast<const uint4*>(sk + tr * 128 + (((2 * c) ^ g) << 4));
-              const uint4 y =
-                  *reinterpret_cast<const uint4*>(sk + tr * 128 + (((2 * c + 1) ^ g) << 4));
-              w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-              w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
-            } else {
-              const uint4 x =
-                  *reinterpret_cast<const uint4*>(sk + tr * 64 + ((c ^ ((g >> 1) & 3)) << 4));
-              w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) t[n][e] = 0.f;
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-              mma_f16(t[n], qa[k], halves(w[k] & 0xFFFFu), halves(w[k] >> 16));
-          }
-          float iv[NG];
-#pragma unroll
-          for (int i = 0; i < NG; ++i) {
-            const float4 sc = s_scale[s * 4 + kw * NG + i];
-            iv[i] = sc.z;
-            const float f0 = qf[0] * sc.x, f1 = qf[1] * sc.x;
-#pragma unroll
-            for (int n = 2 * i; n < 2 * i + 2; ++n) {
-              t[n][0] = fmaf(t[n][0], f0, sc.y);
-              t[n][1] = fmaf(t[n][1], f0, sc.y);
-              t[n][2] = fmaf(t[n][2], f1, sc.y);
-              t[n][3] = fmaf(t[n][3], f1, sc.y);
-            }
-          }
-          if (left < kTile) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if ((kw * NT + n) * 8 + 2 * c + (e & 1) >= left) t[n][e] = -INFINITY;
-          }
-          rescale(t, NT);
-#pragma unroll
-          for (int i = 0; i < NG; ++i) {
-            const float* x = t[2 * i];
-            const float* y = t[2 * i + 1];
-            l[0] = fmaf(iv[i], (x[0] + x[1]) + (y[0] + y[1]), l[0]);
-            l[1] = fmaf(iv[i], (x[2] + x[3]) + (y[2] + y[3]), l[1]);
-            const uint32_t pa[4] = {pack_f16(x[0], x[1]), pack_f16(x[2], x[3]),
-                                    pack_f16(y[0], y[1]), pack_f16(y[2], y[3])};
-            const int tb = (kw * NG + i) * 16 + 2 * c;
-            uint32_t w[4][D / 32];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int tk = tb + (e & 1) + (e >> 1) * 8;
-              if constexpr (D == 128) {
-                const uint4 z =
-                    *reinterpret_cast<const uint4*>(sv + tk * 128 + ((g ^ (tk & 7)) << 4));
-                w[e][0] = z.x, w[e][1] = z.y, w[e][2] = z.z, w[e][3] = z.w;
-              } else {
-                const uint2 z = *reinterpret_cast<const uint2*>(
-                    sv + tk * 64 + (((g >> 1) ^ ((tk >> 1) & 3)) << 4) + (g & 1) * 8);
-                w[e][0] = z.x, w[e][1] = z.y;
-              }
-              // slots behind the sequence may hold anything, NaN too
-              if (left < kTile && tk >= left) {
-#pragma unroll
-                for (int k = 0; k < D / 32; ++k) w[e][k] = 0u;
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-              const uint32_t a0 = __byte_perm(w[0][k], w[1][k], 0x5140);
-              const uint32_t a1 = __byte_perm(w[0][k], w[1][k], 0x7362);
-              const uint32_t b0 = __byte_perm(w[2][k], w[3][k], 0x5140);
-              const uint32_t b1 = __byte_perm(w[2][k], w[3][k], 0x7362);
-              mma_f16(o[4 * k], pa, halves(a0 & 0xFFFFu), halves(b0 & 0xFFFFu));
-              mma_f16(o[4 * k + 1], pa, halves(a0 >> 16), halves(b0 >> 16));
-              mma_f16(o[4 * k + 2], pa, halves(a1 & 0xFFFFu), halves(b1 & 0xFFFFu));
-              mma_f16(o[4 * k + 3], pa, halves(a1 >> 16), halves(b1 >> 16));
-            }
-          }
-        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) sm100::mbar_arrive(&empty[s]);
-      }
-
-      // ---- new tokens: groups of 16, from the last one any row sees down ----
-      if (live && sg.t1 == sg.s.tiles) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t w[D / 8];
-          load_q(i, w);
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            qa[k][i] = w[2 * k];
-            qa[k][i + 2] = w[2 * k + 1];
-          }
-        }
-        const float f = a.scale * kLog2e;
-        const int32_t* par = a.parent ? a.parent + static_cast<size_t>(sg.b) * a.T : nullptr;
-        int cur[2] = {tok[0], tok[1]};  // the next ancestor to mark (trees)
-        const int last = min(r0 + 15, R - 1) / a.G;
-        for (int gi = last / 16; gi >= 0; --gi) {
-          // rows see columns (bits) of this group
-          uint32_t see[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (par) {
-              see[i] = 0u;
-              while (cur[i] >= gi * 16) {
-                see[i] |= 1u << (cur[i] - gi * 16);
-                const int up = __ldg(par + cur[i]);
-                cur[i] = up < cur[i] ? up : -1;  // parents come before their children
-              }
-            } else {
-              const int n = tok[i] - gi * 16 + 1;
-              see[i] = n >= 16 ? 0xFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
-            }
-          }
-          if (gi % KW != kw) continue;
-          float t[2][4];
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int col = min(gi * 16 + n * 8 + g, last);
-            const uint4* p = reinterpret_cast<const uint4*>(
-                a.k_new + ((static_cast<size_t>(sg.b) * a.T + col) * a.Hkv + sg.h) * D +
-                c * (D / 4));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) t[n][e] = 0.f;
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-              const uint4 v = __ldg(p + k);
-              mma_bf16(t[n], qa[2 * k], v.x, v.y);
-              mma_bf16(t[n], qa[2 * k + 1], v.z, v.w);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              t[n][e] = (see[e >> 1] >> (n * 8 + 2 * c + (e & 1))) & 1u ? t[n][e] * f : -INFINITY;
-          }
-          rescale(t, 2);
-          l[0] += (t[0][0] + t[0][1]) + (t[1][0] + t[1][1]);
-          l[1] += (t[0][2] + t[0][3]) + (t[1][2] + t[1][3]);
-          uint32_t w[4][D / 16];
-          bool odd = false;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tk = min(gi * 16 + 2 * c + (e & 1) + (e >> 1) * 8, last);
-            const uint4* p = reinterpret_cast<const uint4*>(
-                a.v_new + ((static_cast<size_t>(sg.b) * a.T + tk) * a.Hkv + sg.h) * D +
-                g * (D / 8));
-#pragma unroll
-            for (int k = 0; k < D / 64; ++k) {
-              const uint4 v = __ldg(p + k);
-              w[e][4 * k] = v.x, w[e][4 * k + 1] = v.y;
-              w[e][4 * k + 2] = v.z, w[e][4 * k + 3] = v.w;
-              odd |= nonfinite2(v.x) || nonfinite2(v.y) || nonfinite2(v.z) || nonfinite2(v.w);
-            }
-          }
-          if (__any_sync(0xFFFFFFFFu, odd)) {
-            // An infinity or NaN among the values: rows that do not see its token
-            // must not meet it (0 times infinity), so this group goes row by row.
-            for (int tk = 0; tk < 16; ++tk) {
-              float pr[2];
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const float x = tk & 1 ? t[0][2 * i + 1] : t[0][2 * i];
-                const float y = tk & 1 ? t[1][2 * i + 1] : t[1][2 * i];
-                pr[i] = __shfl_sync(0xFFFFFFFFu, tk < 8 ? x : y, (lane & 28) | ((tk & 7) >> 1));
-              }
-              if (gi * 16 + tk > last) continue;
-              const uint16_t* p =
-                  a.v_new + ((static_cast<size_t>(sg.b) * a.T + gi * 16 + tk) * a.Hkv + sg.h) * D;
-#pragma unroll
-              for (int j = 0; j < DN; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if ((see[e >> 1] >> tk) & 1u)
-                    o[j][e] = fmaf(pr[e >> 1],
-                                   uno::bf16_bits_to_float(p[(2 * c + (e & 1)) * DN + j]), o[j][e]);
-            }
-          } else {
-            const uint32_t pa[4] = {pack_bf16(t[0][0], t[0][1]), pack_bf16(t[0][2], t[0][3]),
-                                    pack_bf16(t[1][0], t[1][1]), pack_bf16(t[1][2], t[1][3])};
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              mma_bf16(o[2 * k], pa, __byte_perm(w[0][k], w[1][k], 0x5410),
-                       __byte_perm(w[2][k], w[3][k], 0x5410));
-              mma_bf16(o[2 * k + 1], pa, __byte_perm(w[0][k], w[1][k], 0x7632),
-                       __byte_perm(w[2][k], w[3][k], 0x7632));
-            }
-          }
+        if (lane == 0) {
+          sm100::mbar_arrive(&v_full[k2]);
+          sm100::mbar_arrive(&empty[s]);
         }
       }
-
-      // ---- the segment's sums ----
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
-      }
-      if constexpr (KW > 1) {
-        // the token shares of a row meet in shared memory
-        constexpr int kConsumerThreads = 32 * P::kConsumers;
-        auto slot = [&](int k) { return smem + P::kMerge + ((k - 1) * RW + rw) * P::kMergeWarp; };
-        if (kw > 0) {
-          float4* so = reinterpret_cast<float4*>(slot(kw));
-#pragma unroll
-          for (int j = 0; j < DN; ++j)
-            so[j * 32 + lane] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
-          so[DN * 32 + lane] = make_float4(m[0], m[1], l[0], l[1]);
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(kConsumerThreads) : "memory");
-        if (kw == 0) {
-          for (int k = 1; k < KW; ++k) {
-            const float4* so = reinterpret_cast<const float4*>(slot(k));
-            const float4 ml = so[DN * 32 + lane];
-            const float m2[2] = {ml.x, ml.y}, l2[2] = {ml.z, ml.w};
-            float f1[2], f2[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float mx = fmaxf(m[i], m2[i]);
-              f1[i] = m[i] == -INFINITY ? 0.f : uno::ex2(m[i] - mx);
-              f2[i] = m2[i] == -INFINITY ? 0.f : uno::ex2(m2[i] - mx);
-              // a share without a finite maximum still carries its NaN
-              l[i] = (l[i] != l[i] ? l[i] : l[i] * f1[i]) + (l2[i] != l2[i] ? l2[i] : l2[i] * f2[i]);
-              m[i] = mx;
-            }
-#pragma unroll
-            for (int j = 0; j < DN; ++j) {
-              const float4 v = so[j * 32 + lane];
-              o[j][0] = fmaf(v.x, f2[0], o[j][0] * f1[0]);
-              o[j][1] = fmaf(v.y, f2[0], o[j][1] * f1[0]);
-              o[j][2] = fmaf(v.z, f2[1], o[j][2] * f1[1]);
-              o[j][3] = fmaf(v.w, f2[1], o[j][3] * f1[1]);
-            }
-          }
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(kConsumerThreads) : "memory");
-      }
-      if (kw == 0 && live) {
-        if (sg.s.bad) l[0] = l[1] = __uint_as_float(0x7FC00000u);
-        const bool whole = sg.t0 == 0 && sg.t1 == sg.s.tiles;
-        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + (sg.t0 > 0 ? 0 : 1)) * ROWS;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (rows[i] >= R) continue;
-          if (whole) {
-            const float inv = 1.f / l[i];
-            uint4* dst = reinterpret_cast<uint4*>(a.out + q_at[i] + c * (D / 4));
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int k = 0; k < DN / 8; ++k) {
-                const int j = 8 * k, e = 2 * i + n;
-                dst[n * (DN / 8) + k] = make_uint4(
-                    pack_bf16(o[j][e] * inv, o[j + 1][e] * inv),
-                    pack_bf16(o[j + 2][e] * inv, o[j + 3][e] * inv),
-                    pack_bf16(o[j + 4][e] * inv, o[j + 5][e] * inv),
-                    pack_bf16(o[j + 6][e] * inv, o[j + 7][e] * inv));
-              }
-          } else {
-            const size_t row = part + rw * 16 + g + 8 * i;
-            float4* dst = reinterpret_cast<float4*>(a.part_o + row * D + c * (D / 4));
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int k = 0; k < DN / 4; ++k) {
-                const int j = 4 * k, e = 2 * i + n;
-                dst[n * (DN / 4) + k] = make_float4(o[j][e], o[j + 1][e], o[j + 2][e], o[j + 3][e]);
-              }
-            if (c == 0) a.part_ml[row] = make_float2(m[i], l[i]);
-          }
-        }
-      }
-      if (u == u0 && threadIdx.x == 0)
-        a.desc[blockIdx.x] = Desc{sg.start, sg.start + sg.s.tiles, sg.b, sg.h, sg.rt, 0};
-      u = sg.start + sg.t1;
+      u = g.start + g.t1;
     }
+  } else {
+    // ---- softmax: a row per thread ----
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const int my_row = COPIES == 4 ? lane : COPIES == 2 ? (warp & 1) * 32 + lane : threadIdx.x;
+    const int copy = COPIES == 4 ? warp : COPIES == 2 ? warp >> 1 : 0;
+    const int c0 = copy * CW;  // this thread's tokens of a tile
+    int it = 0;
+    bool ok = true;
+    for (long long u = u0; u < u1 && ok;) {
+      const Segment g = segment_at(u);
+      const int r = g.rt * kRows + my_row;  // row of the sequence and KV head
+      const bool valid = r < g.s.nn * a.G;
+      const bool live = __any_sync(0xFFFFFFFFu, valid);
+      float qf = 0.f;
+      {
+        // q 2^sh = hi + lo, its largest magnitude in [128, 256)
+        const int t = valid ? r / a.G : 0;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + ((static_cast<size_t>(g.b) * a.T + t) * a.Hq + g.h * a.G + (r - t * a.G)) * D);
+        uint32_t top = 0;
+        if (valid) {
+#pragma unroll 4
+          for (int k = 0; k < D / 8; ++k) {
+            const uint4 v = __ldg(src + k);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+          }
+        }
+        const int sh = min(7 + 127 - static_cast<int>(top >> 7), 120);
+        const float f = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
+        qf = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+        // an infinite or NaN query saturates in e4m3: its scores are NaN instead
+        if (top >= 0x7F80u) qf = __uint_as_float(0x7FC00000u);
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) {  // 64 elements: 16 columns of each part
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint4 v = valid ? __ldg(src + 8 * k + e) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t h2[4], l2[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float x = bf_lo(w[j]) * f, y = bf_hi(w[j]) * f;
+              h2[j] = e4m3x2(x, y);
+              const float2 back = floats(halves(h2[j]));
+              l2[j] = e4m3x2(x - back.x, y - back.y);
+            }
+            hi[2 * e] = h2[0] | (h2[1] << 16);
+            hi[2 * e + 1] = h2[2] | (h2[3] << 16);
+            lo[2 * e] = l2[0] | (l2[1] << 16);
+            lo[2 * e + 1] = l2[2] | (l2[3] << 16);
+          }
+          tmem_st_x16(tmem + lanes + kColQ + 16 * k, hi);
+          tmem_st_x16(tmem + lanes + kColQ + D / 4 + 16 * k, lo);
+        }
+        sm100::tmem_st_wait();
+        sm100::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(q_full);
+      }
+      float ref = kLowest, l = 0.f;
+      for (int ti = g.t0; ti < g.t1; ++ti, ++it) {
+        const int s = it % kStages, k2 = it & 1;
+        // full[s] too: the scales were written by its arriving thread's warp
+        if (!wait(&full[s], (it / kStages) & 1) || !wait(&s_full[k2], (it >> 1) & 1)) {
+          give_up(kFaultSoftmax);
+          ok = false;
+          break;
+        }
+        sm100::tc_fence_after();
+        const uint32_t st = tmem + lanes + k2 * kTile;
+        if (live) {
+          const int left = g.s.len - ti * kTile - c0;  // of this thread's tokens, those that exist
+          const float4* sc = s_scale + s * (kTile / 16) + c0 / 16;
+          uint32_t pk[CW / 2];  // weights, two to a column
+          float add, top;
+          // weights against the current ref; top: the largest t - ref
+          auto pass = [&](auto whole) {  // whole: all of the thread's tokens exist
+            add = 0.f;
+            top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < CW; c += 32) {
+              uint32_t v[32];
+              sm100::tmem_ld_32x32b_x32(st + c0 + c, v);
+              sm100::tmem_ld_wait();
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float4 x = sc[c / 16 + h];
+                const float f = qf * x.x, off = x.y - ref;
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                  const int i = c + 16 * h + e;
+                  float t0 = fmaf(__uint_as_float(v[16 * h + e]), f, off);
+                  float t1 = fmaf(__uint_as_float(v[16 * h + e + 1]), f, off);
+                  if constexpr (!decltype(whole)::value) {
+                    if (i >= left) t0 = -INFINITY;
+                    if (i + 1 >= left) t1 = -INFINITY;
+                  }
+                  top = fmaxf(top, fmaxf(t0, t1));
+                  t0 = uno::ex2(t0);
+                  t1 = uno::ex2(t1);
+                  sum += t0 + t1;
+                  pk[i / 2] = pack_f16(t0, t1);
+                }
+                add = fmaf(sum, x.z, add);
+              }
+            }
+          };
+          auto weights = [&]() {
+            if (left >= CW) pass(std::true_type{});
+            else pass(std::false_type{});
+          };
+          const bool first = ti == g.t0;
+          if (!first) weights();
+          if (first || __any_sync(0xFFFFFFFFu, top > kLift)) {
+            // ref moves to the tile's largest t, in rows where that is far above it
+            float mx = ref;
+#pragma unroll
+            for (int c = 0; c < CW; c += 32) {
+              uint32_t v[32];
+              sm100::tmem_ld_32x32b_x32(st + c0 + c, v);
+              sm100::tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float4 x = sc[(c + e) / 16];
+                const float t = fmaf(__uint_as_float(v[e]), qf * x.x, x.y);
+                if (c + e < left) mx = fmaxf(mx, t);
+              }
+            }
+            if (!first) {
+              if (!(top > kLift)) mx = ref;
+              const float al = uno::ex2(ref - mx);
+              l *= al;
+              // o holds the tiles before this one once the last of them has been added
+              if (!wait(&o_done[k2 ^ 1], ((it - 1) >> 1) & 1)) {
+                give_up(kFaultSoftmax);
+                ok = false;
+                break;
+              }
+              sm100::tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t v[32];
+                sm100::tmem_ld_32x32b_x32(tmem + lanes + kColO + c, v);
+                sm100::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
+                sm100::tmem_st_32x32b_x32(tmem + lanes + kColO + c, v);
+              }
+            }
+            ref = mx;
+            weights();
+          }
+          l += add;
+          // weights over the scores; the other copies' tokens get weight 0
+#pragma unroll
+          for (int c = 0; c < kTile / 2; c += 16) {
+            if (c >= c0 / 2 && c < c0 / 2 + CW / 2) {
+              tmem_st_x16(st + c, pk + (COPIES == 1 ? c : c % (CW / 2)));
+            } else {
+              const uint32_t z[16] = {};
+              tmem_st_x16(st + c, z);
+            }
+          }
+          sm100::tmem_st_wait();
+        }
+        sm100::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          sm100::mbar_arrive(&p_full[k2]);
+          sm100::mbar_arrive(&empty[s]);
+        }
+      }
+      if (!ok) break;
+      // ---- the segment's sums ----
+      const int last = it - 1;
+      if (!wait(&o_done[last & 1], (last >> 1) & 1)) {
+        give_up(kFaultSoftmax);
+        break;
+      }
+      sm100::tc_fence_after();
+      if (live) {
+        const size_t row =
+            g.t0 == 0 ? ((static_cast<size_t>(g.b) * a.Hkv + g.h) * COPIES + copy) *
+                                (static_cast<size_t>(a.T) * a.G) + r
+                      : static_cast<size_t>(blockIdx.x) * kRows + threadIdx.x;
+        float* dst = (g.t0 == 0 ? a.item_o : a.cta_o) + row * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t v[32];
+          sm100::tmem_ld_32x32b_x32(tmem + lanes + kColO + c, v);
+          sm100::tmem_ld_wait();
+          if (valid) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          }
+        }
+        if (valid) (g.t0 == 0 ? a.item_ml : a.cta_ml)[row] = make_float2(ref, l);
+      }
+      sm100::tc_fence_before();  // o and the queries may be written again
+      u = g.start + g.t1;
+    }
+  }
+  sm100::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    sm100::tc_fence_after();
+    sm100::tmem_dealloc(tmem, 512);
   }
 }
 
-// Items shared by several CTAs: block (i, .) handles the item that CTA i starts
-// in the middle of, when i is the first such CTA of the item. A warp per row.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(128) combine_kernel(const AttnArgs a) {
+// New tokens, and the join with the cached tokens' partial sums. 16 query rows
+// of a sequence and KV head per group of KW warps: the groups of 16 new tokens and
+// the partial sums are dealt to the warps, whose sums meet in shared memory.
+//
+// mma.sync m16n8k16 (bfloat16, weights rounded to bfloat16, 2^-9). A
+// contraction's index needs no particular order, so it is permuted until a
+// lane's share is contiguous: lane (g, c) (g = lane / 4, c = lane % 4) reads keys'
+// elements [c D/4, (c + 1) D/4) of token g, and of values the D/8 elements from
+// g D/8 of the four tokens whose weights it holds from the score fragment.
+template <int D, int KW>
+__global__ void __launch_bounds__(128) finish_kernel(const AttnArgs a) {
+  constexpr int KS = D / 16;  // k-steps of a score
+  constexpr int DN = D / 8;   // output column tiles
+  constexpr int kGroups = 4 / KW;
+  __shared__ float4 s_sum[KW > 1 ? KW - 1 : 1][KW > 1 ? DN + 1 : 1][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kw = warp % KW;
+  const int g = lane >> 2, c = lane & 3;
+  const int rgs = (a.T * a.G + 15) / 16;  // groups of 16 rows
+  const long long item = static_cast<long long>(blockIdx.x) * kGroups + warp / KW;
+  const long long items = static_cast<long long>(a.B) * a.Hkv * rgs;
   uno::launch_dependents();
-  uno::grid_dependency_wait();
-  const Head hd = *a.head;
-  const int i = static_cast<int>(blockIdx.x) + 1;
-  if (i >= hd.ctas) return;
-  auto first_unit = [&](int j) { return hd.units * j / hd.ctas; };
-  const Desc d = a.desc[i];
-  if (first_unit(i) <= d.start || first_unit(i - 1) > d.start) return;
-  const int lane = threadIdx.x & 31;
-  const int rt_row = static_cast<int>(blockIdx.y) * 4 + (threadIdx.x >> 5);  // row of the tile
-  const int nn = a.num_new ? min(max(a.num_new[d.b], 0), a.T) : a.T;
-  const int r = d.rt * ROWS + rt_row;
-  if (r >= nn * a.G) return;
-  // CTA i - 1 began the item (its part's last piece), CTAs i.. go on (their first)
-  int n = 1;
-  while (i - 1 + n < hd.ctas && first_unit(i - 1 + n) < d.end) ++n;
-  auto slot = [&](int k) {
-    return (static_cast<size_t>(i - 1 + k) * 2 + (k == 0 ? 1 : 0)) * ROWS + rt_row;
+  // Every thread waits for cached_kernel before it leaves: the next launch takes
+  // this one's end for cached_kernel's. (Whole warps leave; with KW > 1 whole CTAs.)
+  if (item >= items) {
+    uno::grid_dependency_wait();
+    return;
+  }
+  const int rg = static_cast<int>(item % rgs);
+  const int h = static_cast<int>(item / rgs % a.Hkv);
+  const int b = static_cast<int>(item / rgs / a.Hkv);
+  const Seq sq = seq_of(a, b);
+  const int R = sq.nn * a.G;  // rows of the sequence and head
+  const int r0 = rg * 16;
+  if (r0 >= R) {
+    uno::grid_dependency_wait();
+    return;
+  }
+  const int rows[2] = {r0 + g, r0 + g + 8};
+  // query row r: token r / G, head h G + r % G (rows past the end repeat the last
+  // one, unstored)
+  auto token = [&](int i) { return min(rows[i], R - 1) / a.G; };
+  auto q_at = [&](int i) {
+    const int r = min(rows[i], R - 1), t = r / a.G;
+    return ((static_cast<size_t>(b) * a.T + t) * a.Hq + h * a.G + (r - t * a.G)) * D;
   };
-  constexpr int E = D / 32;  // columns of a lane
-  float acc[E];
+  auto load_q = [&](int i, uint32_t* w) {
+    const uint4* p = reinterpret_cast<const uint4*>(a.q + q_at(i) + c * (D / 4));
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  float mx = -INFINITY;
-  for (int k = lane; k < n; k += 32) mx = fmaxf(mx, a.part_ml[slot(k)].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-  float l = 0.f;
-  for (int k0 = 0; k0 < n; k0 += 32) {
-    float f = 0.f;
-    if (k0 + lane < n) {
-      const float2 ml = a.part_ml[slot(k0 + lane)];
-      f = ml.x == -INFINITY ? 0.f : uno::ex2(ml.x - mx);
-      l += ml.y != ml.y ? ml.y : ml.y * f;  // NaN stays, whatever its reference
+    for (int k = 0; k < D / 32; ++k) {
+      const uint4 v = __ldg(p + k);
+      w[4 * k] = v.x;
+      w[4 * k + 1] = v.y;
+      w[4 * k + 2] = v.z;
+      w[4 * k + 3] = v.w;
     }
-    const int m = min(32, n - k0);
-    for (int k = 0; k < m; ++k) {
-      const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
-      const float* src = a.part_o + slot(k0 + k) * D + lane * E;
-      if constexpr (E == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        acc[0] = fmaf(v.x, fk, acc[0]);
-        acc[1] = fmaf(v.y, fk, acc[1]);
-        acc[2] = fmaf(v.z, fk, acc[2]);
-        acc[3] = fmaf(v.w, fk, acc[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        acc[0] = fmaf(v.x, fk, acc[0]);
-        acc[1] = fmaf(v.y, fk, acc[1]);
+  };
+  uint32_t qa[KS][4];
+  float o[DN][4];
+#pragma unroll
+  for (int i = 0; i < DN; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+  // New reference for t[0..1][..]: weights in place, o and l rescaled.
+  auto rescale = [&](float (*t)[4]) {
+    float mx[2] = {m[0], m[1]};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      mx[0] = fmaxf(mx[0], fmaxf(t[j][0], t[j][1]));
+      mx[1] = fmaxf(mx[1], fmaxf(t[j][2], t[j][3]));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 1));
+      mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 2));
+    }
+    if (__any_sync(0xFFFFFFFFu, mx[0] > m[0] || mx[1] > m[1])) {
+      float al[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        al[i] = m[i] == -INFINITY ? 0.f : uno::ex2(m[i] - mx[i]);
+        l[i] *= al[i];
+        m[i] = mx[i];
+      }
+#pragma unroll
+      for (int j = 0; j < DN; ++j) {
+        o[j][0] *= al[0];
+        o[j][1] *= al[0];
+        o[j][2] *= al[1];
+        o[j][3] *= al[1];
+      }
+    }
+    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[j][e] = uno::ex2(t[j][e] - ref[e >> 1]);
+  };
+
+  // ---- new tokens: groups of 16, from the last one any row sees down ----
+  {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t w[D / 8];
+      load_q(i, w);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        qa[k][i] = w[2 * k];
+        qa[k][i + 2] = w[2 * k + 1];
+      }
+    }
+    const float f = a.scale * kLog2e;
+    const int32_t* par = a.parent ? a.parent + static_cast<size_t>(b) * a.T : nullptr;
+    const int tok[2] = {token(0), token(1)};
+    int cur[2] = {tok[0], tok[1]};  // the next ancestor to mark (trees)
+    const int last = min(r0 + 15, R - 1) / a.G;
+    for (int gi = last / 16; gi >= 0; --gi) {
+      // rows see columns (bits) of this group
+      uint32_t see[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (par) {
+          see[i] = 0u;
+          while (cur[i] >= gi * 16) {
+            see[i] |= 1u << (cur[i] - gi * 16);
+            const int up = __ldg(par + cur[i]);
+            cur[i] = up < cur[i] ? up : -1;  // parents come before their children
+          }
+        } else {
+          const int n = tok[i] - gi * 16 + 1;
+          see[i] = n >= 16 ? 0xFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+        }
+      }
+      if (gi % KW != kw) continue;
+      float t[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int col = min(gi * 16 + n * 8 + g, last);
+        const uint4* p = reinterpret_cast<const uint4*>(
+            a.k_new + ((static_cast<size_t>(b) * a.T + col) * a.Hkv + h) * D +
+            c * (D / 4));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[n][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          const uint4 v = __ldg(p + k);
+          mma_bf16(t[n], qa[2 * k], v.x, v.y);
+          mma_bf16(t[n], qa[2 * k + 1], v.z, v.w);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          t[n][e] = (see[e >> 1] >> (n * 8 + 2 * c + (e & 1))) & 1u ? t[n][e] * f : -INFINITY;
+      }
+      rescale(t);
+      l[0] += (t[0][0] + t[0][1]) + (t[1][0] + t[1][1]);
+      l[1] += (t[0][2] + t[0][3]) + (t[1][2] + t[1][3]);
+      uint32_t pa[4] = {pack_bf16(t[0][0], t[0][1]), pack_bf16(t[0][2], t[0][3]),
+                        pack_bf16(t[1][0], t[1][1]), pack_bf16(t[1][2], t[1][3])};
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k) {  // eight of a lane's columns at a time
+        uint32_t w[4][4];
+        bool odd = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int tk = min(gi * 16 + 2 * c + (e & 1) + (e >> 1) * 8, last);
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(
+              a.v_new + ((static_cast<size_t>(b) * a.T + tk) * a.Hkv + h) * D +
+              g * (D / 8) + 8 * k));
+          w[e][0] = v.x, w[e][1] = v.y, w[e][2] = v.z, w[e][3] = v.w;
+          odd |= nonfinite2(v.x) || nonfinite2(v.y) || nonfinite2(v.z) || nonfinite2(v.w);
+        }
+        if (__any_sync(0xFFFFFFFFu, odd)) {
+          // An infinity or NaN among the values: rows that do not see its token
+          // must not meet it (0 times infinity), so these columns go row by row.
+          for (int tk = 0; tk < 16; ++tk) {
+            float pr[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float x = tk & 1 ? t[0][2 * i + 1] : t[0][2 * i];
+              const float y = tk & 1 ? t[1][2 * i + 1] : t[1][2 * i];
+              pr[i] = __shfl_sync(0xFFFFFFFFu, tk < 8 ? x : y, (lane & 28) | ((tk & 7) >> 1));
+            }
+            if (gi * 16 + tk > last) continue;
+            const uint16_t* p =
+                a.v_new + ((static_cast<size_t>(b) * a.T + gi * 16 + tk) * a.Hkv + h) * D;
+#pragma unroll
+            for (int j = 8 * k; j < 8 * k + 8; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if ((see[e >> 1] >> tk) & 1u)
+                  o[j][e] = fmaf(pr[e >> 1],
+                                 uno::bf16_bits_to_float(p[(2 * c + (e & 1)) * DN + j]),
+                                 o[j][e]);
+          }
+          continue;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int j = 8 * k + 2 * q;
+          mma_bf16(o[j], pa, __byte_perm(w[0][q], w[1][q], 0x5410),
+                   __byte_perm(w[2][q], w[3][q], 0x5410));
+          mma_bf16(o[j + 1], pa, __byte_perm(w[0][q], w[1][q], 0x7632),
+                   __byte_perm(w[2][q], w[3][q], 0x7632));
+        }
       }
     }
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-  const float inv = 1.f / l;
-  uint16_t* dst = a.out +
-                  ((static_cast<size_t>(d.b) * a.T + r / a.G) * a.Hq + d.h * a.G + r % a.G) * D +
-                  lane * E;
-  if constexpr (E == 4)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv),
-                                                pack_bf16(acc[2] * inv, acc[3] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
+  for (int i = 0; i < 2; ++i) {
+    l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
+    l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
+  }
+
+  // ---- partial sums over the cached tokens ----
+  uno::grid_dependency_wait();
+  if (sq.tiles > 0) {
+    const Head hd = *a.head;
+    const int rt = r0 / kRows;
+    const long long start = a.base[b] + static_cast<long long>(h * sq.rts + rt) * sq.tiles;
+    // CTAs [j0, j1) begin inside the item
+    int j0 = static_cast<int>(start * hd.ctas / hd.units);
+    while (j0 < hd.ctas && first_unit(hd, j0) <= start) ++j0;
+    int j1 = j0;
+    while (j1 < hd.ctas && first_unit(hd, j1) < start + sq.tiles) ++j1;
+    const int n = a.copies * (1 + j1 - j0);
+    const int lanes_per_copy = kRows / a.copies;
+    for (int k = kw; k < n; k += KW) {
+      const int cp = k % a.copies, j = k / a.copies;
+      const float2* ml = j == 0 ? a.item_ml : a.cta_ml;
+      const float* po = j == 0 ? a.item_o : a.cta_o;
+      float f1[2], f2[2];
+      const float4* src[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = min(rows[i], R - 1);
+        const size_t at =
+            j == 0 ? ((static_cast<size_t>(b) * a.Hkv + h) * a.copies + cp) *
+                             (static_cast<size_t>(a.T) * a.G) + r
+                   : static_cast<size_t>(j0 + j - 1) * kRows + cp * lanes_per_copy + (r - rt * kRows);
+        const float2 v = ml[at];
+        src[i] = reinterpret_cast<const float4*>(po + at * D + c * (D / 4));
+        const float mx = fmaxf(m[i], v.x);
+        f1[i] = m[i] == -INFINITY ? 0.f : uno::ex2(m[i] - mx);
+        f2[i] = uno::ex2(v.x - mx);
+        // a side without a finite maximum still carries its NaN
+        l[i] = (l[i] != l[i] ? l[i] : l[i] * f1[i]) + (v.y != v.y ? v.y : v.y * f2[i]);
+        m[i] = mx;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)  // columns DN (2 c + q)..
+#pragma unroll
+          for (int e = 0; e < DN / 4; ++e) {
+            const float4 v = src[i][q * (DN / 4) + e];
+            const float w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              o[4 * e + x][2 * i + q] = fmaf(w[x], f2[i], o[4 * e + x][2 * i + q] * f1[i]);
+          }
+    }
+  }
+  if constexpr (KW > 1) {
+    if (kw > 0) {
+#pragma unroll
+      for (int j = 0; j < DN; ++j)
+        s_sum[kw - 1][j][lane] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
+      s_sum[kw - 1][DN][lane] = make_float4(m[0], m[1], l[0], l[1]);
+    }
+    __syncthreads();
+    if (kw > 0) return;
+#pragma unroll 1
+    for (int k = 0; k < KW - 1; ++k) {
+      const float4 ml = s_sum[k][DN][lane];
+      const float m2[2] = {ml.x, ml.y}, l2[2] = {ml.z, ml.w};
+      float f1[2], f2[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float mx = fmaxf(m[i], m2[i]);
+        f1[i] = m[i] == -INFINITY ? 0.f : uno::ex2(m[i] - mx);
+        f2[i] = m2[i] == -INFINITY ? 0.f : uno::ex2(m2[i] - mx);
+        l[i] = (l[i] != l[i] ? l[i] : l[i] * f1[i]) + (l2[i] != l2[i] ? l2[i] : l2[i] * f2[i]);
+        m[i] = mx;
+      }
+#pragma unroll
+      for (int j = 0; j < DN; ++j) {
+        const float4 v = s_sum[k][j][lane];
+        o[j][0] = fmaf(v.x, f2[0], o[j][0] * f1[0]);
+        o[j][1] = fmaf(v.y, f2[0], o[j][1] * f1[0]);
+        o[j][2] = fmaf(v.z, f2[1], o[j][2] * f1[1]);
+        o[j][3] = fmaf(v.w, f2[1], o[j][3] * f1[1]);
+      }
+    }
+  }
+  if (sq.bad) l[0] = l[1] = __uint_as_float(0x7FC00000u);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (rows[i] >= R) continue;
+    const float inv = 1.f / l[i];
+    uint4* dst = reinterpret_cast<uint4*>(a.out + q_at(i) + c * (D / 4));
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int k = 0; k < DN / 8; ++k) {
+        const int j = 8 * k, e = 2 * i + q;
+        dst[q * (DN / 8) + k] =
+            make_uint4(pack_bf16(o[j][e] * inv, o[j + 1][e] * inv),
+                       pack_bf16(o[j + 2][e] * inv, o[j + 3][e] * inv),
+                       pack_bf16(o[j + 4][e] * inv, o[j + 5][e] * inv),
+                       pack_bf16(o[j + 6][e] * inv, o[j + 7][e] * inv));
+      }
+  }
 }
 
 // ---- host side ------------------------------------------------------------------
 
-// Rows per CTA: all of a sequence's rows for one KV head where one tile holds
-// them (in steps of the variants below), else tiles of 128.
-int rows_for(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 80 ? 80 : 128; }
+int copies_for(long long rows) { return rows <= 32 ? 4 : rows <= 64 ? 2 : 1; }
 
 struct Layout {
-  size_t desc, ml, o, bytes;
+  size_t base, item_ml, item_o, cta_ml, cta_o, bytes;
 };
 
-Layout layout(int rows, int D) {
+Layout layout(int B, int T, int Hq, int Hkv, int D) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const long long rows = static_cast<long long>(T) * (Hq / Hkv);
+  const size_t items = static_cast<size_t>(B) * Hkv * rows * copies_for(rows);
+  const size_t lanes = static_cast<size_t>(kMaxCtas) * kRows;
   Layout w;
-  w.desc = 256;
-  w.ml = w.desc + up(sizeof(Desc) * kMaxCtas);
-  w.o = w.ml + up(sizeof(float2) * 2 * kMaxCtas * static_cast<size_t>(rows));
-  w.bytes = w.o + sizeof(float) * 2 * kMaxCtas * static_cast<size_t>(rows) * D;
+  w.base = 256;
+  w.item_ml = w.base + up(sizeof(long long) * B);
+  w.item_o = w.item_ml + up(sizeof(float2) * items);
+  w.cta_ml = w.item_o + up(sizeof(float) * items * D);
+  w.cta_o = w.cta_ml + up(sizeof(float2) * lanes);
+  w.bytes = w.cta_o + sizeof(float) * lanes * D;
   return w;
 }
 
@@ -833,65 +1122,73 @@ bool cache_map(CUtensorMap* map, const void* codes, long long rows, int D, int u
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int RW, int KW>
-int launch(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, cudaStream_t st) {
-  using P = Plan<D, RW, KW>;
-  static std::atomic<uint64_t> attr_done{0};  // devices with the shared-memory opt-in
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return UNO_ERR_CUDA;
-  const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
-  if (!bit || !(attr_done.load(std::memory_order_relaxed) & bit)) {
-    if (cudaFuncSetAttribute(attn_kernel<D, RW, KW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             P::kBytes) != cudaSuccess)
-      return UNO_ERR_CUDA;
-    attr_done.fetch_or(bit, std::memory_order_relaxed);
-  }
-  // a CTA per unit at most, as far as the host can know
-  const long long rts = (static_cast<long long>(a.T) * a.G + P::kRows - 1) / P::kRows;
-  const long long tiles = (static_cast<long long>(a.width) * a.page + kTile - 1) / kTile + 1;
-  long long ctas = std::min<long long>(a.B * rts, kMaxCtas) * a.Hkv;
-  ctas = std::min<long long>(ctas, kMaxCtas) * std::min<long long>(tiles, kMaxCtas);
-  ctas = std::min<long long>(ctas, kMaxCtas / 2 * P::kCtasPerSm);
+template <typename K, typename... Args>
+int launch(K kern, unsigned grid, int threads, int smem, bool early, cudaStream_t st,
+           const Args&... args) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].val.programmaticStreamSerializationAllowed = early;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(P::kThreads);
-  cfg.dynamicSmemBytes = P::kBytes;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, attn_kernel<D, RW, KW>, mk, mv, a) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return UNO_ERR_CUDA;
-  }
-  if (ctas == 1) return UNO_OK;  // nothing is shared
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1), P::kRows / 4);
-  cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = 0;
-  if (cudaLaunchKernelEx(&cfg, combine_kernel<D, P::kRows>, a) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
     (void)cudaGetLastError();
     return UNO_ERR_CUDA;
   }
   return UNO_OK;
 }
 
-template <int D>
-int launch_rows(int rows, const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a,
-                cudaStream_t st) {
-  switch (rows) {
-    case 16: return launch<D, 1, 4>(mk, mv, a, st);
-    case 32: return launch<D, 2, 2>(mk, mv, a, st);
-    case 64: return launch<D, 4, 1>(mk, mv, a, st);
-    case 80: return launch<D, 5, 1>(mk, mv, a, st);
-    default: return launch<D, 8, 1>(mk, mv, a, st);
+template <int D, int COPIES>
+int launch_cached(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a,
+                  cudaStream_t st) {
+  static std::atomic<uint64_t> attr_done{0};  // devices with the shared-memory opt-in
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return UNO_ERR_CUDA;
+  const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
+  if (!bit || !(attr_done.load(std::memory_order_relaxed) & bit)) {
+    if (cudaFuncSetAttribute(cached_kernel<D, COPIES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Plan<D>::kBytes) != cudaSuccess)
+      return UNO_ERR_CUDA;
+    attr_done.fetch_or(bit, std::memory_order_relaxed);
   }
+  // a CTA per unit at most, as far as the host can know
+  const long long rts = (static_cast<long long>(a.T) * a.G + kRows - 1) / kRows;
+  const long long tiles = (static_cast<long long>(a.width) * a.page + kTile - 1) / kTile;
+  long long ctas = std::min<long long>(a.B * rts, kMaxCtas) * a.Hkv;
+  ctas = std::min<long long>(ctas, kMaxCtas) * std::min<long long>(tiles, kMaxCtas);
+  ctas = std::max<long long>(std::min<long long>(ctas, kMaxCtas), 1);
+  return launch(cached_kernel<D, COPIES>, static_cast<unsigned>(ctas), kThreads, Plan<D>::kBytes,
+                true, st, mk, mv, a);
+}
+
+template <int D>
+int launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, bool cached,
+               cudaStream_t st) {
+  if (cached) {
+    const int rc = a.copies == 4   ? launch_cached<D, 4>(mk, mv, a, st)
+                   : a.copies == 2 ? launch_cached<D, 2>(mk, mv, a, st)
+                                   : launch_cached<D, 1>(mk, mv, a, st);
+    if (rc != UNO_OK) return rc;
+  }
+  // (finish_kernel reads its inputs before it waits for the launch before it: it may
+  // start early only behind cached_kernel, which has waited for what wrote them)
+  // four warps per 16 rows while that leaves the GPU room, one when there are many
+  const long long items =
+      static_cast<long long>(a.B) * a.Hkv * ((static_cast<long long>(a.T) * a.G + 15) / 16);
+  if (items <= 4 * kMaxCtas)
+    return launch(finish_kernel<D, 4>, static_cast<unsigned>(items), 128, 0, cached, st, a);
+  return launch(finish_kernel<D, 1>, static_cast<unsigned>((items + 3) / 4), 128, 0, cached, st, a);
 }
 
 bool sizes_ok(int B, int T, int Hq, int Hkv, int D, int page, int width, int num_pages) {
   return uno_host::cache_sizes_ok(B, T, Hkv, D, page, width, num_pages) && T <= 4096 &&
          Hq >= Hkv && Hq % Hkv == 0 && Hq <= 16384 &&
+         static_cast<long long>(B) * Hkv * ((static_cast<long long>(T) * (Hq / Hkv) + 15) / 16) <=
+             0x7FFFFFFFll &&
          static_cast<long long>(num_pages) * Hkv * page <= 0x7FFFFFFFll;
 }
 
@@ -912,7 +1209,7 @@ int attention_fault_flags(bool clear, unsigned* flags) {
 
 extern "C" size_t uno_block_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
   if (!sizes_ok(B, T, Hq, Hkv, D, 64, 0, 0)) return 0;
-  return layout(rows_for(static_cast<long long>(T) * (Hq / Hkv)), D).bytes;
+  return layout(B, T, Hq, Hkv, D).bytes;
 }
 
 extern "C" int uno_block_attention(const void* q, const void* k_new, const void* v_new,
@@ -937,8 +1234,7 @@ extern "C" int uno_block_attention(const void* q, const void* k_new, const void*
                         static_cast<const void*>(num_new), static_cast<const void*>(page_table),
                         static_cast<const void*>(k_scale), static_cast<const void*>(v_scale)})
     if (!uno_host::aligned(p, 4)) return UNO_ERR_ALIGN;
-  const int rows = rows_for(static_cast<long long>(T) * (Hq / Hkv));
-  const Layout w = layout(rows, D);
+  const Layout w = layout(B, T, Hq, Hkv, D);
   if (!workspace || workspace_bytes < w.bytes) return UNO_ERR_WORKSPACE;
   if (!uno_host::aligned(workspace, 16)) return UNO_ERR_ALIGN;
   const int dev = uno_host::check_device();
@@ -965,9 +1261,12 @@ extern "C" int uno_block_attention(const void* q, const void* k_new, const void*
   a.scale = scale;
   char* ws = static_cast<char*>(workspace);
   a.head = reinterpret_cast<Head*>(ws);
-  a.desc = reinterpret_cast<Desc*>(ws + w.desc);
-  a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
-  a.part_o = reinterpret_cast<float*>(ws + w.o);
+  a.base = reinterpret_cast<long long*>(ws + w.base);
+  a.item_ml = reinterpret_cast<float2*>(ws + w.item_ml);
+  a.item_o = reinterpret_cast<float*>(ws + w.item_o);
+  a.cta_ml = reinterpret_cast<float2*>(ws + w.cta_ml);
+  a.cta_o = reinterpret_cast<float*>(ws + w.cta_o);
+  a.copies = copies_for(static_cast<long long>(T) * (Hq / Hkv));
   CUtensorMap mk{}, mv{};
   if (cached) {
     const long long map_rows = static_cast<long long>(num_pages) * Hkv * page;
@@ -976,5 +1275,5 @@ extern "C" int uno_block_attention(const void* q, const void* k_new, const void*
       return UNO_ERR_CUDA;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return D == 128 ? launch_rows<128>(rows, mk, mv, a, st) : launch_rows<64>(rows, mk, mv, a, st);
+  return D == 128 ? launch_all<128>(mk, mv, a, cached, st) : launch_all<64>(mk, mv, a, cached, st);
 }
