@@ -58,9 +58,11 @@ constexpr int kTile = 128;     // cached tokens per unit of work
 constexpr int kRows = 128;     // rows (TMEM lanes) of a tile
 constexpr int kStages = 4;     // tiles of codes in shared memory
 constexpr int kProducers = 2;  // TMA warps, alternating tiles
-// Warps: 0-3 softmax (TMEM lane quarter = warp), 4-7 value decode, then the
-// producers, then the MMA issuer (which owns TMEM).
-constexpr int kFirstProducer = 8;
+// Warps: 0-7 softmax (TMEM lane quarter = warp % 4, half of a row's tokens = warp /
+// 4), 8-11 queries and value decode, then the producers, then the MMA issuer (which
+// owns TMEM).
+constexpr int kFirstDecode = 8;
+constexpr int kFirstProducer = 12;
 constexpr int kMmaWarp = kFirstProducer + kProducers;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kMaxCtas = 148;  // one CTA per SM
@@ -189,12 +191,35 @@ __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity) {
   }
 }
 
-// The whole warp waits (one lane polls).
+// The whole warp waits. The lanes meet first (none may run ahead of one that still
+// has copies to issue) and after (each has seen the phase for itself).
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = wait_one(bar, parity);
   __syncwarp();
-  return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+  const bool ok = wait_one(bar, parity);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
+// The two warps of a TMEM lane quarter meet (they take the same path throughout, on
+// the give-up path too, so neither is ever missing).
+__device__ __forceinline__ void meet(int quarter) {
+  asm volatile("bar.sync %0, 64;" ::"r"(quarter + 1) : "memory");
+}
+
+// TMEM loads and stores of N consecutive columns (one lane per thread).
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
+  static_assert(N == 16 || N == 32, "columns");
+  if constexpr (N == 32) {
+    sm100::tmem_ld_32x32b_x32(taddr, r);
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+  }
 }
 
 // D[tmem] (+)= A[tmem] B[smem desc], one thread. kF8: kind::f8f6f4, else kind::f16.
@@ -215,12 +240,24 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, 
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
+  static_assert(N == 8 || N == 16 || N == 32, "columns");
+  if constexpr (N == 32) {
+    sm100::tmem_st_32x32b_x32(taddr, r);
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]));
+  } else {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
+  }
 }
 
 // Shared-memory descriptors. Codes of a tile of keys: K-major rows of D bytes (one
@@ -248,26 +285,40 @@ __device__ __forceinline__ uint64_t value_desc(uint32_t saddr) {
 }
 
 // Shared memory: [stage]{keys, values}, two tiles of decoded values, scales
-// [stage][16-token group], barriers.
+// [stage][16-token group], the rows' score factors [segment parity][lane], what the
+// two halves of a row tell each other, barriers.
 template <int D>
 struct Plan {
   static constexpr int kStage = 2 * kTile * D;
   static constexpr int kHalfTile = kTile * D * 2;
   static constexpr int kDecoded = kStages * kStage;
   static constexpr int kScales = kDecoded + 2 * kHalfTile;
-  static constexpr int kBars = kScales + kStages * (kTile / 16) * 16;
-  static constexpr int kBytes = kBars + (2 * kStages + 9) * 8 + 8 + 1024;  // + alignment
+  static constexpr int kFactors = kScales + kStages * (kTile / 16) * 16;
+  static constexpr int kTops = kFactors + 2 * kRows * 4;  // [half][lane]
+  static constexpr int kFlags = kTops + 2 * kRows * 4;    // [tile parity][quarter][half]
+  static constexpr int kBars = kFlags + 2 * 4 * 2 * 4;
+  static constexpr int kBytes = kBars + (2 * kStages + 8) * 8 + 8 + 1024;  // + alignment
   static_assert(kBytes <= 232448, "dynamic shared memory per CTA (227 KB)");
 };
+
+// Row of a tile that a TMEM lane holds: with 4 copies of at most 32 rows, with 2 of
+// at most 64.
+template <int COPIES>
+__device__ __forceinline__ int row_of_lane(int lane) {
+  return lane & (kRows / COPIES - 1);
+}
 
 template <int D, int COPIES>
 __global__ void __launch_bounds__(kThreads, 1)
     cached_kernel(const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const AttnArgs a) {
   using P = Plan<D>;
-  constexpr int CW = kTile / COPIES;  // a softmax thread's tokens per tile
+  constexpr int CW = kTile / COPIES;  // a row copy's tokens per tile
+  constexpr int HC = CW / 2;          // a softmax thread's
   // TMEM columns: two score tiles (their weights over them), o, the queries' parts
+  // of two segments
   constexpr uint32_t kColO = 2 * kTile, kColQ = kColO + D;
+  static_assert(kColQ + D <= 512, "TMEM columns");
   constexpr uint32_t kIdescS = (1u << 4) | ((kTile >> 3) << 17) | ((kRows >> 4) << 24);
   constexpr uint32_t kIdescO =
       (1u << 4) | (1u << 16) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((kRows >> 4) << 24);
@@ -278,11 +329,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + P::kBars);  // codes and scales are there
   uint64_t* empty = full + kStages;   // nobody needs them any more
   uint64_t* s_full = empty + kStages; // [2] scores of a tile
-  uint64_t* p_full = s_full + 2;      // [2] weights of a tile
-  uint64_t* v_full = p_full + 2;      // [2] decoded values of a tile
-  uint64_t* o_done = v_full + 2;      // [2] a tile's weighted values are in o
-  uint64_t* q_full = o_done + 2;      // [1] a segment's queries
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(q_full + 1);
+  uint64_t* pv_full = s_full + 2;     // [2] weights and decoded values of a tile
+  uint64_t* o_done = pv_full + 2;     // [2] a tile's weighted values are in o
+  uint64_t* q_full = o_done + 2;      // [2] a segment's queries
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(q_full + 2);
+  float* s_factor = reinterpret_cast<float*>(smem + P::kFactors);
+  float* s_top = reinterpret_cast<float*>(smem + P::kTops);
+  volatile int* s_flag = reinterpret_cast<volatile int*>(smem + P::kFlags);
   __shared__ uint64_t s_end;          // every MMA has completed
   __shared__ long long s_u0, s_u1, s_base;
   __shared__ int s_b;
@@ -292,15 +345,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       sm100::mbar_init(&full[s], 1);
-      sm100::mbar_init(&empty[s], 9);  // softmax and decode warps, the issuer's commit
+      sm100::mbar_init(&empty[s], 13);  // softmax and decode warps, the issuer's commit
     }
     for (int k = 0; k < 2; ++k) {
       sm100::mbar_init(&s_full[k], 1);
-      sm100::mbar_init(&p_full[k], 4);
-      sm100::mbar_init(&v_full[k], 4);
+      sm100::mbar_init(&pv_full[k], 12);  // softmax and decode warps
       sm100::mbar_init(&o_done[k], 1);
+      sm100::mbar_init(&q_full[k], 4);
     }
-    sm100::mbar_init(q_full, 4);
     sm100::mbar_init(&s_end, 1);
     s_abort = 0;
     sm100::fence_mbar_init();
@@ -400,24 +452,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return ok;
       };
-      auto scores = [&](int it) {
+      auto scores = [&](int it, int seg) {
         const int s = it % kStages;
         if (!need(&full[s], (it / kStages) & 1)) return;
         sm100::tc_fence_after();
         const uint64_t kd = key_desc<D>(sm100::smem_addr(smem + s * P::kStage));
         const uint32_t d = tmem + (it & 1) * kTile;
+        const uint32_t q = tmem + kColQ + (seg & 1) * (D / 2);
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int k = 0; k < D / 32; ++k)  // 32 codes: 32 bytes, 8 columns of queries
-            mma_ts<true>(d, tmem + kColQ + part * (D / 4) + 8 * k, kd + 2 * k, kIdescS,
-                         part + k > 0);
+            mma_ts<true>(d, q + part * (D / 4) + 8 * k, kd + 2 * k, kIdescS, part + k > 0);
         sm100::mma_commit(&s_full[it & 1]);
         sm100::mma_commit(&empty[s]);
       };
       auto values = [&](int it, bool first) {
         const int k2 = it & 1;
-        if (!need(&p_full[k2], (it >> 1) & 1) || !need(&v_full[k2], (it >> 1) & 1)) return;
+        if (!need(&pv_full[k2], (it >> 1) & 1)) return;
         sm100::tc_fence_after();
         const uint64_t vd =
             value_desc(sm100::smem_addr(smem + P::kDecoded + k2 * P::kHalfTile));
@@ -427,21 +479,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         !first || k > 0);
         sm100::mma_commit(&o_done[k2]);
       };
+      // Scores run one tile ahead of the weighted values (of the next segment too), in
+      // issue order: tile it + 1's scores overwrite the weights of tile it - 1.
       int it = 0, seg = 0;
+      bool before = false;  // tile it - 1 exists; it began a segment:
+      bool before_first = false;
       for (long long u = u0; u < u1 && ok; ++seg) {
         const Segment g = segment_at(u);
-        const int n = g.t1 - g.t0;
-        // the segment's queries are stored only after its predecessor's o was read
-        if (!need(q_full, seg & 1)) break;
-        sm100::tc_fence_after();
-        scores(it);
-        for (int j = 0; j < n && ok; ++j) {
-          if (j + 1 < n) scores(it + j + 1);  // ahead of this tile's softmax
-          if (ok) values(it + j, j == 0);
+        if (!need(&q_full[seg & 1], (seg >> 1) & 1)) break;
+        for (int j = 0; j < g.t1 - g.t0 && ok; ++j, ++it) {
+          scores(it, seg);
+          if (ok && before) values(it - 1, before_first);
+          before = true;
+          before_first = j == 0;
         }
-        it += n;
         u = g.start + g.t1;
       }
+      if (ok && before) values(it - 1, before_first);
       sm100::mma_commit(&s_end);
       if (!wait_one(&s_end, 0)) give_up(kFaultMma);
     }
@@ -508,13 +562,72 @@ __global__ void __launch_bounds__(kThreads, 1)
     // have given up).
     for (int i = max((ok ? it : mine + 1) - kStages, 0); i <= mine; ++i)
       if (i % kProducers == pr) wait(&full[i % kStages], (i / kStages) & 1);
-  } else if (warp >= 4) {
-    // ---- value decode: codes of a tile to halves ----
-    const int tid = threadIdx.x - 128;
-    int it = 0;
+  } else if (warp >= kFirstDecode) {
+    // ---- queries of a segment to e4m3 parts, codes of a tile's values to halves ----
+    const int tid = threadIdx.x - 32 * kFirstDecode;
+    const uint32_t lanes = static_cast<uint32_t>(tid & 96) << 16;
+    int it = 0, seg = 0;
     bool ok = true;
-    for (long long u = u0; u < u1 && ok;) {
+    for (long long u = u0; u < u1 && ok; ++seg) {
       const Segment g = segment_at(u);
+      // the segment before the last has left the queries' columns (its products are
+      // older than tile it - 2's)
+      if (it >= 2 && !wait(&o_done[it & 1], ((it >> 1) - 1) & 1)) {
+        give_up(kFaultSoftmax);
+        break;
+      }
+      {
+        // q 2^sh = hi + lo, its largest magnitude in [128, 256)
+        const int r = g.rt * kRows + row_of_lane<COPIES>(tid);
+        const bool valid = r < g.s.nn * a.G;
+        const int t = valid ? r / a.G : 0;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + ((static_cast<size_t>(g.b) * a.T + t) * a.Hq + g.h * a.G + (r - t * a.G)) * D);
+        uint32_t top = 0;
+        if (valid) {
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k) {
+            const uint4 v = __ldg(src + k);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+          }
+        }
+        const int sh = min(7 + 127 - static_cast<int>(top >> 7), 120);
+        const float f = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
+        // an infinite or NaN query saturates in e4m3: its scores are NaN instead
+        s_factor[(seg & 1) * kRows + tid] =
+            top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
+                           : a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+        const uint32_t dst = tmem + lanes + kColQ + (seg & 1) * (D / 2);
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) {  // 64 elements: 16 columns of each part
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint4 v = valid ? __ldg(src + 8 * k + e) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t h2[4], l2[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float x = bf_lo(w[j]) * f, y = bf_hi(w[j]) * f;
+              h2[j] = e4m3x2(x, y);
+              const float2 back = floats(halves(h2[j]));
+              l2[j] = e4m3x2(x - back.x, y - back.y);
+            }
+            hi[2 * e] = h2[0] | (h2[1] << 16);
+            hi[2 * e + 1] = h2[2] | (h2[3] << 16);
+            lo[2 * e] = l2[0] | (l2[1] << 16);
+            lo[2 * e + 1] = l2[2] | (l2[3] << 16);
+          }
+          tmem_st<16>(dst + 16 * k, hi);
+          tmem_st<16>(dst + D / 4 + 16 * k, lo);
+        }
+        sm100::tmem_st_wait();
+        sm100::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(&q_full[seg & 1]);
+      }
       for (int ti = g.t0; ti < g.t1; ++ti, ++it) {
         const int s = it % kStages, k2 = it & 1;
         if (!wait(&full[s], (it / kStages) & 1) ||
@@ -549,101 +662,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          sm100::mbar_arrive(&v_full[k2]);
+          sm100::mbar_arrive(&pv_full[k2]);
           sm100::mbar_arrive(&empty[s]);
         }
       }
       u = g.start + g.t1;
     }
   } else {
-    // ---- softmax: a row per thread ----
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const int my_row = COPIES == 4 ? lane : COPIES == 2 ? (warp & 1) * 32 + lane : threadIdx.x;
-    const int copy = COPIES == 4 ? warp : COPIES == 2 ? warp >> 1 : 0;
-    const int c0 = copy * CW;  // this thread's tokens of a tile
-    int it = 0;
-    bool ok = true;
-    for (long long u = u0; u < u1 && ok;) {
+    // ---- softmax: half a row's tokens per thread ----
+    const int quarter = warp & 3, half = warp >> 2;
+    const int tl = quarter * 32 + lane;  // TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const int my_row = row_of_lane<COPIES>(tl);
+    const int copy = COPIES == 4 ? quarter : COPIES == 2 ? quarter >> 1 : 0;
+    const int c0 = copy * CW + half * HC;  // this thread's tokens of a tile
+    constexpr int CH = HC < 32 ? HC : 32;  // of which it loads so many at once
+    int it = 0, seg = 0;
+    bool ok = true;  // false: go on without waiting, the results are abandoned
+    auto need = [&](uint64_t* bar, uint32_t parity) {
+      if (ok && !wait(bar, parity)) {
+        give_up(kFaultSoftmax);
+        ok = false;
+      }
+    };
+    for (long long u = u0; u < u1; ++seg) {
       const Segment g = segment_at(u);
       const int r = g.rt * kRows + my_row;  // row of the sequence and KV head
       const bool valid = r < g.s.nn * a.G;
       const bool live = __any_sync(0xFFFFFFFFu, valid);
-      float qf = 0.f;
-      {
-        // q 2^sh = hi + lo, its largest magnitude in [128, 256)
-        const int t = valid ? r / a.G : 0;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            a.q + ((static_cast<size_t>(g.b) * a.T + t) * a.Hq + g.h * a.G + (r - t * a.G)) * D);
-        uint32_t top = 0;
-        if (valid) {
-#pragma unroll 4
-          for (int k = 0; k < D / 8; ++k) {
-            const uint4 v = __ldg(src + k);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
-          }
-        }
-        const int sh = min(7 + 127 - static_cast<int>(top >> 7), 120);
-        const float f = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
-        qf = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-        // an infinite or NaN query saturates in e4m3: its scores are NaN instead
-        if (top >= 0x7F80u) qf = __uint_as_float(0x7FC00000u);
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k) {  // 64 elements: 16 columns of each part
-          uint32_t hi[16], lo[16];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint4 v = valid ? __ldg(src + 8 * k + e) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t h2[4], l2[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float x = bf_lo(w[j]) * f, y = bf_hi(w[j]) * f;
-              h2[j] = e4m3x2(x, y);
-              const float2 back = floats(halves(h2[j]));
-              l2[j] = e4m3x2(x - back.x, y - back.y);
-            }
-            hi[2 * e] = h2[0] | (h2[1] << 16);
-            hi[2 * e + 1] = h2[2] | (h2[3] << 16);
-            lo[2 * e] = l2[0] | (l2[1] << 16);
-            lo[2 * e + 1] = l2[2] | (l2[3] << 16);
-          }
-          tmem_st_x16(tmem + lanes + kColQ + 16 * k, hi);
-          tmem_st_x16(tmem + lanes + kColQ + D / 4 + 16 * k, lo);
-        }
-        sm100::tmem_st_wait();
-        sm100::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) sm100::mbar_arrive(q_full);
-      }
+      need(&q_full[seg & 1], (seg >> 1) & 1);
+      const float qf = s_factor[(seg & 1) * kRows + tl];
       float ref = kLowest, l = 0.f;
       for (int ti = g.t0; ti < g.t1; ++ti, ++it) {
         const int s = it % kStages, k2 = it & 1;
         // full[s] too: the scales were written by its arriving thread's warp
-        if (!wait(&full[s], (it / kStages) & 1) || !wait(&s_full[k2], (it >> 1) & 1)) {
-          give_up(kFaultSoftmax);
-          ok = false;
-          break;
-        }
+        need(&full[s], (it / kStages) & 1);
+        need(&s_full[k2], (it >> 1) & 1);
         sm100::tc_fence_after();
         const uint32_t st = tmem + lanes + k2 * kTile;
         if (live) {
           const int left = g.s.len - ti * kTile - c0;  // of this thread's tokens, those that exist
           const float4* sc = s_scale + s * (kTile / 16) + c0 / 16;
-          uint32_t pk[CW / 2];  // weights, two to a column
+          uint32_t pk[HC / 2];  // weights, two to a column
           float add, top;
           // weights against the current ref; top: the largest t - ref
           auto pass = [&](auto whole) {  // whole: all of the thread's tokens exist
             add = 0.f;
             top = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < CW; c += 32) {
-              uint32_t v[32];
-              sm100::tmem_ld_32x32b_x32(st + c0 + c, v);
+            for (int c = 0; c < HC; c += CH) {
+              uint32_t v[CH];
+              tmem_ld<CH>(st + c0 + c, v);
               sm100::tmem_ld_wait();
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
+              for (int h = 0; h < CH / 16; ++h) {
                 const float4 x = sc[c / 16 + h];
                 const float f = qf * x.x, off = x.y - ref;
                 float sum = 0.f;
@@ -667,39 +739,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           };
           auto weights = [&]() {
-            if (left >= CW) pass(std::true_type{});
+            if (left >= HC) pass(std::true_type{});
             else pass(std::false_type{});
           };
+          // A ref moves when either half of a row of the quarter asks for it (the
+          // flags alternate with the tiles, so a meeting later they may be rewritten).
           const bool first = ti == g.t0;
-          if (!first) weights();
-          if (first || __any_sync(0xFFFFFFFFu, top > kLift)) {
-            // ref moves to the tile's largest t, in rows where that is far above it
-            float mx = ref;
+          bool move = first;
+          if (!first) {
+            weights();
+            const bool ask = __any_sync(0xFFFFFFFFu, top > kLift);
+            if (lane == 0) s_flag[(k2 * 4 + quarter) * 2 + half] = ask;
+            meet(quarter);
+            move = ask || s_flag[(k2 * 4 + quarter) * 2 + (half ^ 1)];
+          }
+          if (move) {
+            // to the tile's largest t, in rows where that is far above it
+            float mx = kLowest;
 #pragma unroll
-            for (int c = 0; c < CW; c += 32) {
-              uint32_t v[32];
-              sm100::tmem_ld_32x32b_x32(st + c0 + c, v);
+            for (int c = 0; c < HC; c += CH) {
+              uint32_t v[CH];
+              tmem_ld<CH>(st + c0 + c, v);
               sm100::tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
+              for (int e = 0; e < CH; ++e) {
                 const float4 x = sc[(c + e) / 16];
                 const float t = fmaf(__uint_as_float(v[e]), qf * x.x, x.y);
                 if (c + e < left) mx = fmaxf(mx, t);
               }
             }
-            if (!first) {
-              if (!(top > kLift)) mx = ref;
-              const float al = uno::ex2(ref - mx);
+            s_top[half * kRows + tl] = mx;
+            meet(quarter);
+            mx = fmaxf(mx, s_top[(half ^ 1) * kRows + tl]);
+            meet(quarter);  // read before a next move writes
+            if (first) {
+              ref = mx;
+            } else {
+              const float to = mx > ref + kLift ? mx : ref;
+              const float al = uno::ex2(ref - to);
+              ref = to;
               l *= al;
-              // o holds the tiles before this one once the last of them has been added
-              if (!wait(&o_done[k2 ^ 1], ((it - 1) >> 1) & 1)) {
-                give_up(kFaultSoftmax);
-                ok = false;
-                break;
-              }
+              // o holds the tiles before this one once the last of them has been added;
+              // each half rescales half of its columns
+              need(&o_done[k2 ^ 1], ((it - 1) >> 1) & 1);
               sm100::tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
+              for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
                 uint32_t v[32];
                 sm100::tmem_ld_32x32b_x32(tmem + lanes + kColO + c, v);
                 sm100::tmem_ld_wait();
@@ -708,45 +793,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sm100::tmem_st_32x32b_x32(tmem + lanes + kColO + c, v);
               }
             }
-            ref = mx;
             weights();
+            // both halves have read the scores that the weights overwrite
+            meet(quarter);
           }
           l += add;
-          // weights over the scores; the other copies' tokens get weight 0
+          tmem_st<HC / 2>(st + c0 / 2, pk);
+          if constexpr (COPIES > 1) {
+            // the other copies' tokens get weight 0: 16-column blocks, the halves
+            // taking every other one
 #pragma unroll
-          for (int c = 0; c < kTile / 2; c += 16) {
-            if (c >= c0 / 2 && c < c0 / 2 + CW / 2) {
-              tmem_st_x16(st + c, pk + (COPIES == 1 ? c : c % (CW / 2)));
-            } else {
-              const uint32_t z[16] = {};
-              tmem_st_x16(st + c, z);
-            }
+            for (int k = 0; k < 4; ++k)
+              if ((k & 1) == half && k / (4 / COPIES) != copy) {
+                const uint32_t z[16] = {};
+                tmem_st<16>(st + 16 * k, z);
+              }
           }
           sm100::tmem_st_wait();
         }
         sm100::tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          sm100::mbar_arrive(&p_full[k2]);
+          sm100::mbar_arrive(&pv_full[k2]);
           sm100::mbar_arrive(&empty[s]);
         }
       }
-      if (!ok) break;
       // ---- the segment's sums ----
       const int last = it - 1;
-      if (!wait(&o_done[last & 1], (last >> 1) & 1)) {
-        give_up(kFaultSoftmax);
-        break;
-      }
+      need(&o_done[last & 1], (last >> 1) & 1);
       sm100::tc_fence_after();
       if (live) {
         const size_t row =
             g.t0 == 0 ? ((static_cast<size_t>(g.b) * a.Hkv + g.h) * COPIES + copy) *
                                 (static_cast<size_t>(a.T) * a.G) + r
-                      : static_cast<size_t>(blockIdx.x) * kRows + threadIdx.x;
+                      : static_cast<size_t>(blockIdx.x) * kRows + tl;
         float* dst = (g.t0 == 0 ? a.item_o : a.cta_o) + row * D;
+        if (half == 1) s_top[kRows + tl] = l;
+        meet(quarter);
+        if (half == 0 && valid)
+          (g.t0 == 0 ? a.item_ml : a.cta_ml)[row] = make_float2(ref, l + s_top[kRows + tl]);
+        meet(quarter);
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
           uint32_t v[32];
           sm100::tmem_ld_32x32b_x32(tmem + lanes + kColO + c, v);
           sm100::tmem_ld_wait();
@@ -756,9 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
           }
         }
-        if (valid) (g.t0 == 0 ? a.item_ml : a.cta_ml)[row] = make_float2(ref, l);
       }
-      sm100::tc_fence_before();  // o and the queries may be written again
+      sm100::tc_fence_before();  // o may be written again
       u = g.start + g.t1;
     }
   }
