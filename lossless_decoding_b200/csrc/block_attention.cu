@@ -15,10 +15,10 @@
 // stay under the 1420 clocks in which an SM's share of the bandwidth brings it.
 //
 // Split. The work items are (sequence, KV head, tile of 128 query rows), each a
-// list of 128-token tiles of the cache. The tiles of all items form one line
-// that the CTAs share out evenly, whatever the lengths of the sequences, so a
-// CTA's part starts and ends inside items. (Lengths are on the device: a split
-// planned on the host would have to assume the longest.)
+// list of 128-token tiles of the cache. The items form one line, each as long as
+// its tiles and kLead units for its start, that the CTAs share out evenly, whatever
+// the lengths of the sequences; a CTA's part starts and ends inside items. (Lengths
+// are on the device: a split planned on the host would have to assume the longest.)
 //
 // Products. tcgen05, rows on the 128 TMEM lanes. Scores: kind::f8f6f4 on the codes
 // as they are; the queries are split into two e4m3 parts, q 2^s = hi + lo
@@ -68,6 +68,7 @@ constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kMaxCtas = 148;  // one CTA per SM
 constexpr long long kWaitClocks = 2000000000ll;  // bound of every wait: about a second
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kLead = 2;       // units that an item's start counts for, in tiles
 constexpr float kLift = 8.f;   // log2 of how far a weight may pass 1 before its row's ref moves
 // Floor of a row's ref: a tile without a finite score leaves it there.
 constexpr float kLowest = -3.0e38f;
@@ -76,7 +77,7 @@ enum : unsigned { kFaultProducer = 8u, kFaultMma = 16u, kFaultSoftmax = 32u };
 __device__ unsigned int g_attn_fault;
 
 struct Head {
-  long long units;  // tiles of all items
+  long long units;  // of all items
   int ctas;         // CTAs that have a part
 };
 
@@ -109,7 +110,7 @@ struct AttnArgs {
 struct Seq {
   int len;    // cached tokens (0 when invalid)
   int nn;     // new tokens
-  int tiles;  // units per item
+  int tiles;  // per item
   int rts;    // row tiles
   bool bad;   // length outside the page table: the rows come out as NaN
   long long units;
@@ -123,7 +124,7 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
   s.nn = a.num_new ? min(max(a.num_new[b], 0), a.T) : a.T;
   s.tiles = (s.len + kTile - 1) / kTile;
   s.rts = (s.nn * a.G + kRows - 1) / kRows;
-  s.units = static_cast<long long>(a.Hkv) * s.rts * s.tiles;
+  s.units = s.tiles ? static_cast<long long>(a.Hkv) * s.rts * (s.tiles + kLead) : 0;
   return s;
 }
 
@@ -415,8 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // A segment: the part of one item that this CTA does.
   struct Segment {
     Seq s;
-    int b, h, rt, t0, t1;  // tiles [t0, t1) of the item
-    long long start;       // the item's first unit
+    int b, h, rt, t0, t1;  // tiles [t0, t1) of the item (none, when it has only lead units)
+    long long end;         // the line's unit behind the segment
   };
   long long base = s_base;
   int b = s_b;
@@ -428,13 +429,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       g.s = seq_of(a, ++b);
     }
     g.b = b;
-    const int item = static_cast<int>((u - base) / g.s.tiles);
-    g.start = base + static_cast<long long>(item) * g.s.tiles;
-    g.t0 = static_cast<int>(u - g.start);
-    g.t1 = static_cast<int>(min(u1 - g.start, static_cast<long long>(g.s.tiles)));
+    const int len = g.s.tiles + kLead;
+    const long long rel = u - base;
+    const int item = rel < 0x7FFFFFFF ? static_cast<int>(rel) / len : static_cast<int>(rel / len);
+    const long long start = base + static_cast<long long>(item) * len;
+    g.end = min(u1, start + len);
+    g.t0 = max(static_cast<int>(u - start) - kLead, 0);
+    g.t1 = max(static_cast<int>(g.end - start) - kLead, 0);
     g.h = item / g.s.rts;
     g.rt = item - g.h * g.s.rts;
     return g;
+  };
+  // The next segment with tiles at or behind u (u behind it on return); false at the end.
+  auto next_segment = [&](long long& u, Segment& g) {
+    while (u < u1) {
+      g = segment_at(u);
+      u = g.end;
+      if (g.t1 > g.t0) return true;
+    }
+    return false;
   };
   auto give_up = [&](unsigned bit) {
     if (lane == 0) atomicOr(&g_attn_fault, bit);
@@ -479,23 +492,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         !first || k > 0);
         sm100::mma_commit(&o_done[k2]);
       };
-      // Scores run one tile ahead of the weighted values (of the next segment too), in
-      // issue order: tile it + 1's scores overwrite the weights of tile it - 1.
+      // Scores run one tile ahead of the weighted values, in issue order: tile
+      // it + 1's scores overwrite the weights of tile it - 1.
       int it = 0, seg = 0;
-      bool before = false;  // tile it - 1 exists; it began a segment:
-      bool before_first = false;
-      for (long long u = u0; u < u1 && ok; ++seg) {
-        const Segment g = segment_at(u);
+      Segment g;
+      for (long long u = u0; ok && next_segment(u, g); ++seg) {
+        const int n = g.t1 - g.t0;
         if (!need(&q_full[seg & 1], (seg >> 1) & 1)) break;
-        for (int j = 0; j < g.t1 - g.t0 && ok; ++j, ++it) {
-          scores(it, seg);
-          if (ok && before) values(it - 1, before_first);
-          before = true;
-          before_first = j == 0;
+        scores(it, seg);
+        for (int j = 0; j < n && ok; ++j, ++it) {
+          if (j + 1 < n) scores(it + 1, seg);
+          if (ok) values(it, j == 0);
         }
-        u = g.start + g.t1;
       }
-      if (ok && before) values(it - 1, before_first);
       sm100::mma_commit(&s_end);
       if (!wait_one(&s_end, 0)) give_up(kFaultMma);
     }
@@ -507,8 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int it = 0;                           // tiles of this CTA so far, over all segments
     int mine = -1;                        // this warp's last tile
     bool ok = true;
-    for (long long u = u0; u < u1 && ok;) {
-      const Segment g = segment_at(u);
+    Segment g;
+    for (long long u = u0; ok && next_segment(u, g);) {
       const int n = g.t1 - g.t0;
       // 32 / per of this warp's tiles at a time: page ids and scales of all their
       // copies in one round of loads, a copy per lane
@@ -555,7 +564,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       it += n;
-      u = g.start + g.t1;
     }
     // No copy may still be landing when the CTA exits: wait for this warp's
     // among the last kStages tiles (their readers have done so too, unless they
@@ -568,8 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(tid & 96) << 16;
     int it = 0, seg = 0;
     bool ok = true;
-    for (long long u = u0; u < u1 && ok; ++seg) {
-      const Segment g = segment_at(u);
+    Segment g;
+    for (long long u = u0; ok && next_segment(u, g); ++seg) {
       // the segment before the last has left the queries' columns (its products are
       // older than tile it - 2's)
       if (it >= 2 && !wait(&o_done[it & 1], ((it >> 1) - 1) & 1)) {
@@ -583,16 +591,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = valid ? r / a.G : 0;
         const uint4* src = reinterpret_cast<const uint4*>(
             a.q + ((static_cast<size_t>(g.b) * a.T + t) * a.Hq + g.h * a.G + (r - t * a.G)) * D);
+        uint32_t w[D / 2];
         uint32_t top = 0;
-        if (valid) {
 #pragma unroll
-          for (int k = 0; k < D / 8; ++k) {
-            const uint4 v = __ldg(src + k);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
-          }
+        for (int k = 0; k < D / 8; ++k) {
+          const uint4 v = valid ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+          w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
         }
+#pragma unroll
+        for (int k = 0; k < D / 2; ++k) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
         const int sh = min(7 + 127 - static_cast<int>(top >> 7), 120);
         const float f = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
         // an infinite or NaN query saturates in e4m3: its scores are NaN instead
@@ -604,21 +611,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < D / 64; ++k) {  // 64 elements: 16 columns of each part
           uint32_t hi[16], lo[16];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint4 v = valid ? __ldg(src + 8 * k + e) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t h2[4], l2[4];
+          for (int e = 0; e < 16; ++e) {
+            uint32_t h2[2], l2[2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float x = bf_lo(w[j]) * f, y = bf_hi(w[j]) * f;
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t two = w[32 * k + 2 * e + j];
+              const float x = bf_lo(two) * f, y = bf_hi(two) * f;
               h2[j] = e4m3x2(x, y);
               const float2 back = floats(halves(h2[j]));
               l2[j] = e4m3x2(x - back.x, y - back.y);
             }
-            hi[2 * e] = h2[0] | (h2[1] << 16);
-            hi[2 * e + 1] = h2[2] | (h2[3] << 16);
-            lo[2 * e] = l2[0] | (l2[1] << 16);
-            lo[2 * e + 1] = l2[2] | (l2[3] << 16);
+            hi[e] = h2[0] | (h2[1] << 16);
+            lo[e] = l2[0] | (l2[1] << 16);
           }
           tmem_st<16>(dst + 16 * k, hi);
           tmem_st<16>(dst + D / 4 + 16 * k, lo);
@@ -666,7 +670,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           sm100::mbar_arrive(&empty[s]);
         }
       }
-      u = g.start + g.t1;
     }
   } else {
     // ---- softmax: half a row's tokens per thread ----
@@ -676,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int my_row = row_of_lane<COPIES>(tl);
     const int copy = COPIES == 4 ? quarter : COPIES == 2 ? quarter >> 1 : 0;
     const int c0 = copy * CW + half * HC;  // this thread's tokens of a tile
-    constexpr int CH = HC < 32 ? HC : 32;  // of which it loads so many at once
+    constexpr int CH = 16;  // of which it loads so many at once
     int it = 0, seg = 0;
     bool ok = true;  // false: go on without waiting, the results are abandoned
     auto need = [&](uint64_t* bar, uint32_t parity) {
@@ -685,8 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = false;
       }
     };
-    for (long long u = u0; u < u1; ++seg) {
-      const Segment g = segment_at(u);
+    Segment g;
+    for (long long u = u0; next_segment(u, g); ++seg) {
       const int r = g.rt * kRows + my_row;  // row of the sequence and KV head
       const bool valid = r < g.s.nn * a.G;
       const bool live = __any_sync(0xFFFFFFFFu, valid);
@@ -709,33 +712,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto pass = [&](auto whole) {  // whole: all of the thread's tokens exist
             add = 0.f;
             top = -INFINITY;
+            uint32_t v[2][CH];  // a chunk ahead
+            tmem_ld<CH>(st + c0, v[0]);
 #pragma unroll
-            for (int c = 0; c < HC; c += CH) {
-              uint32_t v[CH];
-              tmem_ld<CH>(st + c0 + c, v);
+            for (int k = 0; k < HC / CH; ++k) {
               sm100::tmem_ld_wait();
+              if (k + 1 < HC / CH) tmem_ld<CH>(st + c0 + (k + 1) * CH, v[(k + 1) & 1]);
+              const float4 x = sc[k];
+              const float f = qf * x.x, off = x.y - ref;
+              float sum = 0.f;
 #pragma unroll
-              for (int h = 0; h < CH / 16; ++h) {
-                const float4 x = sc[c / 16 + h];
-                const float f = qf * x.x, off = x.y - ref;
-                float sum = 0.f;
-#pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                  const int i = c + 16 * h + e;
-                  float t0 = fmaf(__uint_as_float(v[16 * h + e]), f, off);
-                  float t1 = fmaf(__uint_as_float(v[16 * h + e + 1]), f, off);
-                  if constexpr (!decltype(whole)::value) {
-                    if (i >= left) t0 = -INFINITY;
-                    if (i + 1 >= left) t1 = -INFINITY;
-                  }
-                  top = fmaxf(top, fmaxf(t0, t1));
-                  t0 = uno::ex2(t0);
-                  t1 = uno::ex2(t1);
-                  sum += t0 + t1;
-                  pk[i / 2] = pack_f16(t0, t1);
+              for (int e = 0; e < CH; e += 2) {
+                const int i = k * CH + e;
+                float t0 = fmaf(__uint_as_float(v[k & 1][e]), f, off);
+                float t1 = fmaf(__uint_as_float(v[k & 1][e + 1]), f, off);
+                if constexpr (!decltype(whole)::value) {
+                  if (i >= left) t0 = -INFINITY;
+                  if (i + 1 >= left) t1 = -INFINITY;
                 }
-                add = fmaf(sum, x.z, add);
+                top = fmaxf(top, fmaxf(t0, t1));
+                t0 = uno::ex2(t0);
+                t1 = uno::ex2(t1);
+                sum += t0 + t1;
+                pk[i / 2] = pack_f16(t0, t1);
               }
+              add = fmaf(sum, x.z, add);
             }
           };
           auto weights = [&]() {
@@ -763,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               sm100::tmem_ld_wait();
 #pragma unroll
               for (int e = 0; e < CH; ++e) {
-                const float4 x = sc[(c + e) / 16];
+                const float4 x = sc[c / CH];
                 const float t = fmaf(__uint_as_float(v[e]), qf * x.x, x.y);
                 if (c + e < left) mx = fmaxf(mx, t);
               }
@@ -846,7 +847,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       sm100::tc_fence_before();  // o may be written again
-      u = g.start + g.t1;
     }
   }
   sm100::tc_fence_before();
@@ -1077,12 +1077,12 @@ __global__ void __launch_bounds__(128) finish_kernel(const AttnArgs a) {
   if (sq.tiles > 0) {
     const Head hd = *a.head;
     const int rt = r0 / kRows;
-    const long long start = a.base[b] + static_cast<long long>(h * sq.rts + rt) * sq.tiles;
-    // CTAs [j0, j1) begin inside the item
+    const long long start = a.base[b] + static_cast<long long>(h * sq.rts + rt) * (sq.tiles + kLead);
+    // CTAs [j0, j1) begin inside the item's tiles
     int j0 = static_cast<int>(start * hd.ctas / hd.units);
-    while (j0 < hd.ctas && first_unit(hd, j0) <= start) ++j0;
+    while (j0 < hd.ctas && first_unit(hd, j0) <= start + kLead) ++j0;
     int j1 = j0;
-    while (j1 < hd.ctas && first_unit(hd, j1) < start + sq.tiles) ++j1;
+    while (j1 < hd.ctas && first_unit(hd, j1) < start + kLead + sq.tiles) ++j1;
     const int n = a.copies * (1 + j1 - j0);
     const int lanes_per_copy = kRows / a.copies;
     for (int k = kw; k < n; k += KW) {
