@@ -192,12 +192,16 @@ __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity) {
   }
 }
 
-// The whole warp waits. The lanes meet first (none may run ahead of one that still
-// has copies to issue) and after (each has seen the phase for itself).
+// The whole warp waits. The lanes poll together: none runs ahead of one that still
+// has copies to issue, and each has seen the phase for itself.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
   __syncwarp();
-  const bool ok = wait_one(bar, parity);
-  return __all_sync(0xFFFFFFFFu, ok);
+  if (__all_sync(0xFFFFFFFFu, sm100::mbar_try_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  for (uint32_t it = 1;; ++it) {
+    if (__all_sync(0xFFFFFFFFu, sm100::mbar_try_wait(bar, parity))) return true;
+    if ((it & 63u) == 0 && __any_sync(0xFFFFFFFFu, clock64() - t0 > kWaitClocks)) return false;
+  }
 }
 
 // The two warps of a TMEM lane quarter meet (they take the same path throughout, on
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float4* s_scale = reinterpret_cast<float4*>(smem + P::kScales);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + P::kBars);  // codes and scales are there
   uint64_t* empty = full + kStages;   // nobody needs them any more
-  uint64_t* s_full = empty + kStages; // [2] scores of a tile
+  uint64_t* s_full = empty + kStages; // [2] scores and scales of a tile
   uint64_t* pv_full = s_full + 2;     // [2] weights and decoded values of a tile
   uint64_t* o_done = pv_full + 2;     // [2] a tile's weighted values are in o
   uint64_t* q_full = o_done + 2;      // [2] a segment's queries
@@ -349,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm100::mbar_init(&empty[s], 13);  // softmax and decode warps, the issuer's commit
     }
     for (int k = 0; k < 2; ++k) {
-      sm100::mbar_init(&s_full[k], 1);
+      sm100::mbar_init(&s_full[k], 5);  // the issuer's commit, decode warps
       sm100::mbar_init(&pv_full[k], 12);  // softmax and decode warps
       sm100::mbar_init(&o_done[k], 1);
       sm100::mbar_init(&q_full[k], 4);
@@ -640,6 +644,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
+        // the scales that full[s] came with are the softmax warps' to read, too
+        if (lane == 0) sm100::mbar_arrive(&s_full[k2]);
         const uint8_t* src = smem + s * P::kStage + kTile * D;
         uint8_t* dst = smem + P::kDecoded + k2 * P::kHalfTile;
         const int left = g.s.len - ti * kTile;
@@ -698,8 +704,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       float ref = kLowest, l = 0.f;
       for (int ti = g.t0; ti < g.t1; ++ti, ++it) {
         const int s = it % kStages, k2 = it & 1;
-        // full[s] too: the scales were written by its arriving thread's warp
-        need(&full[s], (it / kStages) & 1);
         need(&s_full[k2], (it >> 1) & 1);
         sm100::tc_fence_after();
         const uint32_t st = tmem + lanes + k2 * kTile;
@@ -739,64 +743,60 @@ __global__ void __launch_bounds__(kThreads, 1)
               add = fmaf(sum, x.z, add);
             }
           };
-          auto weights = [&]() {
-            if (left >= HC) pass(std::true_type{});
-            else pass(std::false_type{});
-          };
           // A ref moves when either half of a row of the quarter asks for it (the
           // flags alternate with the tiles, so a meeting later they may be rewritten).
-          const bool first = ti == g.t0;
-          bool move = first;
-          if (!first) {
-            weights();
-            const bool ask = __any_sync(0xFFFFFFFFu, top > kLift);
-            if (lane == 0) s_flag[(k2 * 4 + quarter) * 2 + half] = ask;
-            meet(quarter);
-            move = ask || s_flag[(k2 * 4 + quarter) * 2 + (half ^ 1)];
-          }
-          if (move) {
-            // to the tile's largest t, in rows where that is far above it
-            float mx = kLowest;
-#pragma unroll
-            for (int c = 0; c < HC; c += CH) {
-              uint32_t v[CH];
-              tmem_ld<CH>(st + c0 + c, v);
-              sm100::tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < CH; ++e) {
-                const float4 x = sc[c / CH];
-                const float t = fmaf(__uint_as_float(v[e]), qf * x.x, x.y);
-                if (c + e < left) mx = fmaxf(mx, t);
-              }
-            }
-            s_top[half * kRows + tl] = mx;
-            meet(quarter);
-            mx = fmaxf(mx, s_top[(half ^ 1) * kRows + tl]);
-            meet(quarter);  // read before a next move writes
-            if (first) {
-              ref = mx;
-            } else {
-              const float to = mx > ref + kLift ? mx : ref;
-              const float al = uno::ex2(ref - to);
-              ref = to;
-              l *= al;
-              // o holds the tiles before this one once the last of them has been added;
-              // each half rescales half of its columns
-              need(&o_done[k2 ^ 1], ((it - 1) >> 1) & 1);
-              sm100::tc_fence_after();
+          bool move = ti == g.t0;  // the first tile sets it
+          for (;;) {
+            if (move) {
+              // to the tile's largest t, in rows where that is far above it
+              float mx = kLowest;
 #pragma unroll 1
-              for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
-                uint32_t v[32];
-                sm100::tmem_ld_32x32b_x32(tmem + lanes + kColO + c, v);
+              for (int k = 0; k < HC / CH; ++k) {
+                uint32_t v[CH];
+                tmem_ld<CH>(st + c0 + k * CH, v);
                 sm100::tmem_ld_wait();
+                const float4 x = sc[k];
+                const float f = qf * x.x;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
-                sm100::tmem_st_32x32b_x32(tmem + lanes + kColO + c, v);
+                for (int e = 0; e < CH; ++e) {
+                  const float t = fmaf(__uint_as_float(v[e]), f, x.y);
+                  if (k * CH + e < left) mx = fmaxf(mx, t);
+                }
+              }
+              s_top[half * kRows + tl] = mx;
+              meet(quarter);
+              mx = fmaxf(mx, s_top[(half ^ 1) * kRows + tl]);
+              meet(quarter);  // read before a next move writes
+              if (ti == g.t0) {
+                ref = mx;
+              } else {
+                const float to = mx > ref + kLift ? mx : ref;
+                const float al = uno::ex2(ref - to);
+                ref = to;
+                l *= al;
+                // o holds the tiles before this one once the last of them has been added;
+                // each half rescales half of its columns
+                need(&o_done[k2 ^ 1], ((it - 1) >> 1) & 1);
+                sm100::tc_fence_after();
+#pragma unroll 1
+                for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
+                  uint32_t v[32];
+                  sm100::tmem_ld_32x32b_x32(tmem + lanes + kColO + c, v);
+                  sm100::tmem_ld_wait();
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
+                  sm100::tmem_st_32x32b_x32(tmem + lanes + kColO + c, v);
+                }
               }
             }
-            weights();
-            // both halves have read the scores that the weights overwrite
-            meet(quarter);
+            if (left >= HC) pass(std::true_type{});
+            else pass(std::false_type{});
+            const bool ask = !move && __any_sync(0xFFFFFFFFu, top > kLift);
+            if (lane == 0) s_flag[(k2 * 4 + quarter) * 2 + half] = ask;
+            meet(quarter);  // both halves have read the scores that the weights overwrite
+            if (move) break;
+            move = ask || s_flag[(k2 * 4 + quarter) * 2 + (half ^ 1)];
+            if (!move) break;
           }
           l += add;
           tmem_st<HC / 2>(st + c0 / 2, pk);
