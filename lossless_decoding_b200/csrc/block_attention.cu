@@ -58,14 +58,15 @@ constexpr int kTile = 128;     // cached tokens per unit of work
 constexpr int kRows = 128;     // rows (TMEM lanes) of a tile
 constexpr int kStages = 4;     // tiles of codes in shared memory
 constexpr int kProducers = 2;  // TMA warps, alternating tiles
-// Warps: 0-7 softmax (TMEM lane quarter = warp % 4, half of a row's tokens = warp /
-// 4), 8-11 queries and value decode, then the producers, then the MMA issuer (which
-// owns TMEM).
-constexpr int kFirstDecode = 8;
-constexpr int kFirstProducer = 12;
-constexpr int kMmaWarp = kFirstProducer + kProducers;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+// Warps of cached_kernel: 4 parts() for the softmax (TMEM lane quarter = warp % 4, part
+// of a row's tokens = warp / 4), 4 for queries and value decode, the producers, and
+// two MMA issuers (scores; weighted values): a thread that has issued products
+// waits at its next barrier until they are done, so one issuer would leave the
+// tensor pipe idle between the two.
+__host__ __device__ constexpr int parts(int copies) { return copies == 1 ? 4 : 2; }
+constexpr int threads(int copies) { return 32 * (4 * parts(copies) + 4 + kProducers + 2); }
 constexpr int kMaxCtas = 148;  // one CTA per SM
+constexpr int kMaxT = 4096;    // new tokens per sequence
 constexpr long long kWaitClocks = 2000000000ll;  // bound of every wait: about a second
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kLead = 2;       // units that an item's start counts for, in tiles
@@ -181,14 +182,27 @@ __device__ __forceinline__ float2 floats(uint32_t halves2) {
   return f;
 }
 
+__device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(sm100::smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // One thread waits for the phase with the given parity, giving up after about a
-// second (false then).
+// second (false then). It polls with test_wait: try_wait may suspend the thread, and
+// waking it took 500 to 600 clocks of a tile's 1900.
 __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity) {
-  if (sm100::mbar_try_wait(bar, parity)) return true;
+  if (phase_done(bar, parity)) return true;
   const long long t0 = clock64();
   for (uint32_t it = 1;; ++it) {
-    if (sm100::mbar_try_wait(bar, parity)) return true;
-    if ((it & 63u) == 0 && clock64() - t0 > kWaitClocks) return false;
+    if (phase_done(bar, parity)) return true;
+    if ((it & 255u) == 0 && clock64() - t0 > kWaitClocks) return false;
   }
 }
 
@@ -196,18 +210,19 @@ __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity) {
 // has copies to issue, and each has seen the phase for itself.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
   __syncwarp();
-  if (__all_sync(0xFFFFFFFFu, sm100::mbar_try_wait(bar, parity))) return true;
+  if (__all_sync(0xFFFFFFFFu, phase_done(bar, parity))) return true;
   const long long t0 = clock64();
   for (uint32_t it = 1;; ++it) {
-    if (__all_sync(0xFFFFFFFFu, sm100::mbar_try_wait(bar, parity))) return true;
-    if ((it & 63u) == 0 && __any_sync(0xFFFFFFFFu, clock64() - t0 > kWaitClocks)) return false;
+    if (__all_sync(0xFFFFFFFFu, phase_done(bar, parity))) return true;
+    if ((it & 255u) == 0 && __any_sync(0xFFFFFFFFu, clock64() - t0 > kWaitClocks)) return false;
   }
 }
 
-// The two warps of a TMEM lane quarter meet (they take the same path throughout, on
-// the give-up path too, so neither is ever missing).
+// The softmax warps of a TMEM lane quarter meet (they take the same path throughout,
+// on the give-up path too, so none is ever missing).
+template <int PARTS>
 __device__ __forceinline__ void meet(int quarter) {
-  asm volatile("bar.sync %0, 64;" ::"r"(quarter + 1) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(quarter + 1), "n"(32 * PARTS) : "memory");
 }
 
 // TMEM loads and stores of N consecutive columns (one lane per thread).
@@ -291,7 +306,7 @@ __device__ __forceinline__ uint64_t value_desc(uint32_t saddr) {
 
 // Shared memory: [stage]{keys, values}, two tiles of decoded values, scales
 // [stage][16-token group], the rows' score factors [segment parity][lane], what the
-// two halves of a row tell each other, barriers.
+// parts of a row tell each other, barriers.
 template <int D>
 struct Plan {
   static constexpr int kStage = 2 * kTile * D;
@@ -299,9 +314,9 @@ struct Plan {
   static constexpr int kDecoded = kStages * kStage;
   static constexpr int kScales = kDecoded + 2 * kHalfTile;
   static constexpr int kFactors = kScales + kStages * (kTile / 16) * 16;
-  static constexpr int kTops = kFactors + 2 * kRows * 4;  // [half][lane]
-  static constexpr int kFlags = kTops + 2 * kRows * 4;    // [tile parity][quarter][half]
-  static constexpr int kBars = kFlags + 2 * 4 * 2 * 4;
+  static constexpr int kTops = kFactors + 2 * kRows * 4;  // [part][lane]
+  static constexpr int kFlags = kTops + 4 * kRows * 4;    // [tile parity][quarter][part]
+  static constexpr int kBars = kFlags + 2 * 4 * 4 * 4;
   static constexpr int kBytes = kBars + (2 * kStages + 8) * 8 + 8 + 1024;  // + alignment
   static_assert(kBytes <= 232448, "dynamic shared memory per CTA (227 KB)");
 };
@@ -314,12 +329,15 @@ __device__ __forceinline__ int row_of_lane(int lane) {
 }
 
 template <int D, int COPIES>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads(COPIES), 1)
     cached_kernel(const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const AttnArgs a) {
   using P = Plan<D>;
   constexpr int CW = kTile / COPIES;  // a row copy's tokens per tile
-  constexpr int HC = CW / 2;          // a softmax thread's
+  constexpr int PARTS = parts(COPIES);
+  constexpr int HC = CW / PARTS;      // a softmax thread's
+  constexpr int kFirstDecode = 4 * PARTS, kFirstProducer = kFirstDecode + 4;
+  constexpr int kMmaWarp = kFirstProducer + kProducers;  // scores (and TMEM); + 1: values
   // TMEM columns: two score tiles (their weights over them), o, the queries' parts
   // of two segments
   constexpr uint32_t kColO = 2 * kTile, kColQ = kColO + D;
@@ -350,15 +368,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       sm100::mbar_init(&full[s], 1);
-      sm100::mbar_init(&empty[s], 13);  // softmax and decode warps, the issuer's commit
+      sm100::mbar_init(&empty[s], 4 * PARTS + 5);  // softmax and decode warps, a commit
     }
     for (int k = 0; k < 2; ++k) {
       sm100::mbar_init(&s_full[k], 5);  // the issuer's commit, decode warps
-      sm100::mbar_init(&pv_full[k], 12);  // softmax and decode warps
+      sm100::mbar_init(&pv_full[k], 4 * PARTS + 4);  // softmax and decode warps
       sm100::mbar_init(&o_done[k], 1);
       sm100::mbar_init(&q_full[k], 4);
     }
-    sm100::mbar_init(&s_end, 1);
+    sm100::mbar_init(&s_end, 2);  // one commit per issuer
     s_abort = 0;
     sm100::fence_mbar_init();
   }
@@ -458,8 +476,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_abort = 1;
   };
 
-  if (warp == kMmaWarp) {
-    // ---- MMA issuer ----
+  if (warp >= kMmaWarp) {
+    // ---- MMA issuers ----
     if (lane == 0) {
       bool ok = true;
       auto need = [&](uint64_t* bar, uint32_t parity) {
@@ -471,6 +489,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto scores = [&](int it, int seg) {
         const int s = it % kStages;
+        // the tile's columns held the weights of tile it - 2
+        if (it >= 2 && !need(&o_done[it & 1], ((it >> 1) - 1) & 1)) return;
         if (!need(&full[s], (it / kStages) & 1)) return;
         sm100::tc_fence_after();
         const uint64_t kd = key_desc<D>(sm100::smem_addr(smem + s * P::kStage));
@@ -496,17 +516,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         !first || k > 0);
         sm100::mma_commit(&o_done[k2]);
       };
-      // Scores run one tile ahead of the weighted values, in issue order: tile
-      // it + 1's scores overwrite the weights of tile it - 1.
       int it = 0, seg = 0;
       Segment g;
       for (long long u = u0; ok && next_segment(u, g); ++seg) {
-        const int n = g.t1 - g.t0;
-        if (!need(&q_full[seg & 1], (seg >> 1) & 1)) break;
-        scores(it, seg);
-        for (int j = 0; j < n && ok; ++j, ++it) {
-          if (j + 1 < n) scores(it + 1, seg);
-          if (ok) values(it, j == 0);
+        if (warp == kMmaWarp && !need(&q_full[seg & 1], (seg >> 1) & 1)) break;
+        for (int j = 0; j < g.t1 - g.t0 && ok; ++j, ++it) {
+          if (warp == kMmaWarp) scores(it, seg);
+          else values(it, j == 0);
         }
       }
       sm100::mma_commit(&s_end);
@@ -678,13 +694,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ---- softmax: half a row's tokens per thread ----
-    const int quarter = warp & 3, half = warp >> 2;
+    // ---- softmax: a part of a row's tokens per thread ----
+    const int quarter = warp & 3, part = warp >> 2;
     const int tl = quarter * 32 + lane;  // TMEM lane
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const int my_row = row_of_lane<COPIES>(tl);
     const int copy = COPIES == 4 ? quarter : COPIES == 2 ? quarter >> 1 : 0;
-    const int c0 = copy * CW + half * HC;  // this thread's tokens of a tile
+    const int c0 = copy * CW + part * HC;  // this thread's tokens of a tile
     constexpr int CH = 16;  // of which it loads so many at once
     int it = 0, seg = 0;
     bool ok = true;  // false: go on without waiting, the results are abandoned
@@ -743,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               add = fmaf(sum, x.z, add);
             }
           };
-          // A ref moves when either half of a row of the quarter asks for it (the
+          // A ref moves when any part of a row of the quarter asks for it (the
           // flags alternate with the tiles, so a meeting later they may be rewritten).
           bool move = ti == g.t0;  // the first tile sets it
           for (;;) {
@@ -763,10 +779,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                   if (k * CH + e < left) mx = fmaxf(mx, t);
                 }
               }
-              s_top[half * kRows + tl] = mx;
-              meet(quarter);
-              mx = fmaxf(mx, s_top[(half ^ 1) * kRows + tl]);
-              meet(quarter);  // read before a next move writes
+              s_top[part * kRows + tl] = mx;
+              meet<PARTS>(quarter);
+#pragma unroll
+              for (int k = 0; k < PARTS; ++k) mx = fmaxf(mx, s_top[k * kRows + tl]);
+              meet<PARTS>(quarter);  // read before a next move writes
               if (ti == g.t0) {
                 ref = mx;
               } else {
@@ -775,37 +792,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ref = to;
                 l *= al;
                 // o holds the tiles before this one once the last of them has been added;
-                // each half rescales half of its columns
+                // each part rescales its share of the columns
                 need(&o_done[k2 ^ 1], ((it - 1) >> 1) & 1);
                 sm100::tc_fence_after();
 #pragma unroll 1
-                for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
-                  uint32_t v[32];
-                  sm100::tmem_ld_32x32b_x32(tmem + lanes + kColO + c, v);
+                for (int c = part * (D / PARTS); c < (part + 1) * (D / PARTS); c += 16) {
+                  uint32_t v[16];
+                  tmem_ld<16>(tmem + lanes + kColO + c, v);
                   sm100::tmem_ld_wait();
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
-                  sm100::tmem_st_32x32b_x32(tmem + lanes + kColO + c, v);
+                  for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
+                  tmem_st<16>(tmem + lanes + kColO + c, v);
                 }
               }
             }
             if (left >= HC) pass(std::true_type{});
             else pass(std::false_type{});
             const bool ask = !move && __any_sync(0xFFFFFFFFu, top > kLift);
-            if (lane == 0) s_flag[(k2 * 4 + quarter) * 2 + half] = ask;
-            meet(quarter);  // both halves have read the scores that the weights overwrite
+            if (lane == 0) s_flag[(k2 * 4 + quarter) * 4 + part] = ask;
+            meet<PARTS>(quarter);  // all parts have read the scores that the weights overwrite
             if (move) break;
-            move = ask || s_flag[(k2 * 4 + quarter) * 2 + (half ^ 1)];
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) move |= s_flag[(k2 * 4 + quarter) * 4 + k] != 0;
             if (!move) break;
           }
           l += add;
           tmem_st<HC / 2>(st + c0 / 2, pk);
           if constexpr (COPIES > 1) {
-            // the other copies' tokens get weight 0: 16-column blocks, the halves
+            // the other copies' tokens get weight 0: 16-column blocks, the parts
             // taking every other one
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if ((k & 1) == half && k / (4 / COPIES) != copy) {
+              if ((k & 1) == part && k / (4 / COPIES) != copy) {
                 const uint32_t z[16] = {};
                 tmem_st<16>(st + 16 * k, z);
               }
@@ -829,19 +847,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 (static_cast<size_t>(a.T) * a.G) + r
                       : static_cast<size_t>(blockIdx.x) * kRows + tl;
         float* dst = (g.t0 == 0 ? a.item_o : a.cta_o) + row * D;
-        if (half == 1) s_top[kRows + tl] = l;
-        meet(quarter);
-        if (half == 0 && valid)
-          (g.t0 == 0 ? a.item_ml : a.cta_ml)[row] = make_float2(ref, l + s_top[kRows + tl]);
-        meet(quarter);
+        s_top[part * kRows + tl] = l;
+        meet<PARTS>(quarter);
+        if (part == 0 && valid) {
+#pragma unroll
+          for (int k = 1; k < PARTS; ++k) l += s_top[k * kRows + tl];
+          (g.t0 == 0 ? a.item_ml : a.cta_ml)[row] = make_float2(ref, l);
+        }
+        meet<PARTS>(quarter);
 #pragma unroll 1
-        for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
-          uint32_t v[32];
-          sm100::tmem_ld_32x32b_x32(tmem + lanes + kColO + c, v);
+        for (int c = part * (D / PARTS); c < (part + 1) * (D / PARTS); c += 16) {
+          uint32_t v[16];
+          tmem_ld<16>(tmem + lanes + kColO + c, v);
           sm100::tmem_ld_wait();
           if (valid) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
+            for (int e = 0; e < 16; e += 4)
               *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
           }
         }
@@ -867,11 +888,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // elements [c D/4, (c + 1) D/4) of token g, and of values the D/8 elements from
 // g D/8 of the four tokens whose weights it holds from the score fragment.
 template <int D, int KW>
-__global__ void __launch_bounds__(128) finish_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(128, 2) finish_kernel(const AttnArgs a) {
   constexpr int KS = D / 16;  // k-steps of a score
   constexpr int DN = D / 8;   // output column tiles
   constexpr int kGroups = 4 / KW;
   __shared__ float4 s_sum[KW > 1 ? KW - 1 : 1][KW > 1 ? DN + 1 : 1][32];
+  __shared__ int16_t s_parent[kGroups][kMaxT];  // of the item's sequence
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kw = warp % KW;
   const int g = lane >> 2, c = lane & 3;
@@ -971,7 +993,20 @@ __global__ void __launch_bounds__(128) finish_kernel(const AttnArgs a) {
       }
     }
     const float f = a.scale * kLog2e;
-    const int32_t* par = a.parent ? a.parent + static_cast<size_t>(b) * a.T : nullptr;
+    const bool tree = a.parent != nullptr;
+    int16_t* par = s_parent[KW > 1 ? 0 : warp];
+    if (tree) {
+      // up to the last of these rows' tokens; parents come before their children, any
+      // other value ends the chain
+      const int32_t* src = a.parent + static_cast<size_t>(b) * a.T;
+      const int n = min(r0 + 15, R - 1) / a.G + 1;
+      for (int t = KW > 1 ? threadIdx.x : lane; t < n; t += 32 * KW) {
+        const int up = __ldg(src + t);
+        par[t] = static_cast<int16_t>(up < t ? max(up, -1) : -1);
+      }
+      if (KW > 1) __syncthreads();
+      else __syncwarp();
+    }
     const int tok[2] = {token(0), token(1)};
     int cur[2] = {tok[0], tok[1]};  // the next ancestor to mark (trees)
     const int last = min(r0 + 15, R - 1) / a.G;
@@ -980,12 +1015,11 @@ __global__ void __launch_bounds__(128) finish_kernel(const AttnArgs a) {
       uint32_t see[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (par) {
+        if (tree) {
           see[i] = 0u;
           while (cur[i] >= gi * 16) {
             see[i] |= 1u << (cur[i] - gi * 16);
-            const int up = __ldg(par + cur[i]);
-            cur[i] = up < cur[i] ? up : -1;  // parents come before their children
+            cur[i] = par[cur[i]];
           }
         } else {
           const int n = tok[i] - gi * 16 + 1;
@@ -993,20 +1027,33 @@ __global__ void __launch_bounds__(128) finish_kernel(const AttnArgs a) {
         }
       }
       if (gi % KW != kw) continue;
-      float t[2][4];
+      // the group's keys and values in one round of loads
+      uint4 kv[2][D / 32], vv[4][D / 64];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         const int col = min(gi * 16 + n * 8 + g, last);
         const uint4* p = reinterpret_cast<const uint4*>(
-            a.k_new + ((static_cast<size_t>(b) * a.T + col) * a.Hkv + h) * D +
-            c * (D / 4));
+            a.k_new + ((static_cast<size_t>(b) * a.T + col) * a.Hkv + h) * D + c * (D / 4));
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) kv[n][k] = __ldg(p + k);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int tk = min(gi * 16 + 2 * c + (e & 1) + (e >> 1) * 8, last);
+        const uint4* p = reinterpret_cast<const uint4*>(
+            a.v_new + ((static_cast<size_t>(b) * a.T + tk) * a.Hkv + h) * D + g * (D / 8));
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) vv[e][k] = __ldg(p + k);
+      }
+      float t[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) t[n][e] = 0.f;
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
-          const uint4 v = __ldg(p + k);
-          mma_bf16(t[n], qa[2 * k], v.x, v.y);
-          mma_bf16(t[n], qa[2 * k + 1], v.z, v.w);
+          mma_bf16(t[n], qa[2 * k], kv[n][k].x, kv[n][k].y);
+          mma_bf16(t[n], qa[2 * k + 1], kv[n][k].z, kv[n][k].w);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -1023,10 +1070,7 @@ __global__ void __launch_bounds__(128) finish_kernel(const AttnArgs a) {
         bool odd = false;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int tk = min(gi * 16 + 2 * c + (e & 1) + (e >> 1) * 8, last);
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(
-              a.v_new + ((static_cast<size_t>(b) * a.T + tk) * a.Hkv + h) * D +
-              g * (D / 8) + 8 * k));
+          const uint4 v = vv[e][k];
           w[e][0] = v.x, w[e][1] = v.y, w[e][2] = v.z, w[e][3] = v.w;
           odd |= nonfinite2(v.x) || nonfinite2(v.y) || nonfinite2(v.z) || nonfinite2(v.w);
         }
@@ -1248,7 +1292,7 @@ int launch_cached(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& 
   long long ctas = std::min<long long>(a.B * rts, kMaxCtas) * a.Hkv;
   ctas = std::min<long long>(ctas, kMaxCtas) * std::min<long long>(tiles, kMaxCtas);
   ctas = std::max<long long>(std::min<long long>(ctas, kMaxCtas), 1);
-  return launch(cached_kernel<D, COPIES>, static_cast<unsigned>(ctas), kThreads, Plan<D>::kBytes,
+  return launch(cached_kernel<D, COPIES>, static_cast<unsigned>(ctas), threads(COPIES), Plan<D>::kBytes,
                 true, st, mk, mv, a);
 }
 
@@ -1272,7 +1316,7 @@ int launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, 
 }
 
 bool sizes_ok(int B, int T, int Hq, int Hkv, int D, int page, int width, int num_pages) {
-  return uno_host::cache_sizes_ok(B, T, Hkv, D, page, width, num_pages) && T <= 4096 &&
+  return uno_host::cache_sizes_ok(B, T, Hkv, D, page, width, num_pages) && T <= kMaxT &&
          Hq >= Hkv && Hq % Hkv == 0 && Hq <= 16384 &&
          static_cast<long long>(B) * Hkv * ((static_cast<long long>(T) * (Hq / Hkv) + 15) / 16) <=
              0x7FFFFFFFll &&
