@@ -69,6 +69,7 @@ constexpr int kMaxCtas = 148;  // one CTA per SM
 constexpr int kMaxT = 4096;    // new tokens per sequence
 constexpr long long kWaitClocks = 2000000000ll;  // bound of every wait: about a second
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kCachedSeqs = 512;  // sequences whose sizes a CTA keeps in shared memory
 constexpr int kLead = 2;       // units that an item's start counts for, in tiles
 constexpr float kLift = 8.f;   // log2 of how far a weight may pass 1 before its row's ref moves
 // Floor of a row's ref: a tile without a finite score leaves it there.
@@ -76,11 +77,6 @@ constexpr float kLowest = -3.0e38f;
 
 enum : unsigned { kFaultProducer = 8u, kFaultMma = 16u, kFaultSoftmax = 32u };
 __device__ unsigned int g_attn_fault;
-
-struct Head {
-  long long units;  // of all items
-  int ctas;         // CTAs that have a part
-};
 
 struct AttnArgs {
   const uint16_t* q;      // [B][T][Hq][D]
@@ -96,11 +92,10 @@ struct AttnArgs {
   int B, T, Hq, Hkv, G, page, width, num_pages;
   int copies;             // of the rows on the lanes: 4, 2 or 1
   float scale;            // softmax scale
-  // workspace
-  Head* head;
-  long long* base;        // [B] first unit of each sequence
-  // partial sums of parts that begin an item: [B][Hkv][copies][T G], and of those
-  // that begin inside one (a CTA's first): [CTA][128 lanes]
+  // workspace: partial sums of parts that begin an item, [B][Hkv][copies][T G], and
+  // of those that begin inside one (a CTA's first), [CTA][128 lanes]; per item
+  // [B][Hkv][row tiles] the CTAs of the latter, (first, how many)
+  int2* item_ctas;
   float2* item_ml;        // (ref, normaliser)
   float* item_o;          // [..][D]
   float2* cta_ml;
@@ -117,20 +112,20 @@ struct Seq {
   long long units;
 };
 
-__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
+__device__ __forceinline__ Seq seq_from(const AttnArgs& a, int len, int num_new) {
   Seq s;
-  s.len = a.lens[b];
+  s.len = len;
   s.bad = s.len < 0 || s.len > a.width * a.page;
   if (s.bad) s.len = 0;
-  s.nn = a.num_new ? min(max(a.num_new[b], 0), a.T) : a.T;
+  s.nn = min(max(num_new, 0), a.T);
   s.tiles = (s.len + kTile - 1) / kTile;
   s.rts = (s.nn * a.G + kRows - 1) / kRows;
   s.units = s.tiles ? static_cast<long long>(a.Hkv) * s.rts * (s.tiles + kLead) : 0;
   return s;
 }
 
-__device__ __forceinline__ long long first_unit(const Head& h, int cta) {
-  return h.units * cta / h.ctas;
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
+  return seq_from(a, a.lens[b], a.num_new ? a.num_new[b] : a.T);
 }
 
 __device__ __forceinline__ void mma_bf16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -360,8 +355,9 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
   float* s_top = reinterpret_cast<float*>(smem + P::kTops);
   volatile int* s_flag = reinterpret_cast<volatile int*>(smem + P::kFlags);
   __shared__ uint64_t s_end;          // every MMA has completed
-  __shared__ long long s_u0, s_u1, s_base;
-  __shared__ int s_b;
+  __shared__ long long s_total, s_u0, s_u1, s_base;
+  __shared__ int s_b, s_ctas;
+  __shared__ int s_size[2][kCachedSeqs];  // cached and new tokens
   __shared__ volatile int s_abort;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -385,11 +381,22 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
   // finish_kernel may start: what it reads before its own wait is older than this launch
   uno::launch_dependents();
 
+  const bool small = a.B <= kCachedSeqs;
+  if (small) {
+    for (int i = threadIdx.x; i < a.B; i += blockDim.x) {
+      s_size[0][i] = a.lens[i];
+      s_size[1][i] = a.num_new ? a.num_new[i] : a.T;
+    }
+    __syncthreads();
+  }
+  auto seq = [&](int i) {
+    return small ? seq_from(a, s_size[0][i], s_size[1][i]) : seq_of(a, i);
+  };
   // This CTA's part [u0, u1) of the line, and the sequence it starts in.
   if (warp == 0) {
     long long total = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-      long long n = b0 + lane < a.B ? seq_of(a, b0 + lane).units : 0;
+      long long n = b0 + lane < a.B ? seq(b0 + lane).units : 0;
 #pragma unroll
       for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
       total += n;
@@ -398,35 +405,32 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
     const int i = blockIdx.x;
     const long long u0 = i < ctas ? total * i / ctas : total;
     const long long u1 = i < ctas ? total * (i + 1) / ctas : total;
-    long long base = 0, my_base = 0;
+    long long base = 0;
     int at = 0;
-    if (u0 < u1 || i == 0) {
-      bool found = u0 >= u1;
-      for (int b0 = 0; b0 < a.B && !(found && i != 0); b0 += 32) {
-        const long long n = b0 + lane < a.B ? seq_of(a, b0 + lane).units : 0;
-        long long pre = n;  // inclusive prefix over the lanes
+    for (int b0 = 0; u0 < u1; b0 += 32) {  // ends: u0 < total
+      const long long n = b0 + lane < a.B ? seq(b0 + lane).units : 0;
+      long long pre = n;  // inclusive prefix over the lanes
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long up = __shfl_up_sync(0xFFFFFFFFu, pre, o);
-          if (lane >= o) pre += up;
-        }
-        if (i == 0 && b0 + lane < a.B) a.base[b0 + lane] = base + pre - n;
-        const unsigned in = __ballot_sync(0xFFFFFFFFu, u0 < base + pre);
-        if (in && !found) {
-          const int l = __ffs(in) - 1;
-          my_base = base + __shfl_sync(0xFFFFFFFFu, pre - n, l);
-          at = b0 + l;
-          found = true;
-        }
-        base += __shfl_sync(0xFFFFFFFFu, pre, 31);
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xFFFFFFFFu, pre, o);
+        if (lane >= o) pre += up;
       }
+      const unsigned in = __ballot_sync(0xFFFFFFFFu, u0 < base + pre);
+      if (in) {
+        const int l = __ffs(in) - 1;
+        base += __shfl_sync(0xFFFFFFFFu, pre - n, l);
+        at = b0 + l;
+        break;
+      }
+      base += __shfl_sync(0xFFFFFFFFu, pre, 31);
     }
     if (lane == 0) {
+      s_total = total;
+      s_ctas = ctas;
       s_u0 = u0;
       s_u1 = u1;
-      s_base = my_base;
+      s_base = base;
       s_b = at;
-      if (i == 0) *a.head = Head{total, ctas};
     }
   }
   sm100::tc_fence_before();
@@ -439,23 +443,25 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
   struct Segment {
     Seq s;
     int b, h, rt, t0, t1;  // tiles [t0, t1) of the item (none, when it has only lead units)
-    long long end;         // the line's unit behind the segment
+    long long end;         // the line's unit behind the segment, and behind the item
+    long long item_end;
   };
   long long base = s_base;
   int b = s_b;
   auto segment_at = [&](long long u) {
     Segment g;
-    g.s = seq_of(a, b);
+    g.s = seq(b);
     while (u >= base + g.s.units) {
       base += g.s.units;
-      g.s = seq_of(a, ++b);
+      g.s = seq(++b);
     }
     g.b = b;
     const int len = g.s.tiles + kLead;
     const long long rel = u - base;
     const int item = rel < 0x7FFFFFFF ? static_cast<int>(rel) / len : static_cast<int>(rel / len);
     const long long start = base + static_cast<long long>(item) * len;
-    g.end = min(u1, start + len);
+    g.item_end = start + len;
+    g.end = min(u1, g.item_end);
     g.t0 = max(static_cast<int>(u - start) - kLead, 0);
     g.t1 = max(static_cast<int>(g.end - start) - kLead, 0);
     g.h = item / g.s.rts;
@@ -594,64 +600,69 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
     // ---- queries of a segment to e4m3 parts, codes of a tile's values to halves ----
     const int tid = threadIdx.x - 32 * kFirstDecode;
     const uint32_t lanes = static_cast<uint32_t>(tid & 96) << 16;
+    // The queries of segment `seg`, in the columns that those of segment seg - 2 have left.
+    auto stage_queries = [&](const Segment& g, int seg) {
+      // q 2^sh = hi + lo, its largest magnitude in [128, 256)
+      const int r = g.rt * kRows + row_of_lane<COPIES>(tid);
+      const bool valid = r < g.s.nn * a.G;
+      const int t = valid ? r / a.G : 0;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.q + ((static_cast<size_t>(g.b) * a.T + t) * a.Hq + g.h * a.G + (r - t * a.G)) * D);
+      uint32_t top = 0;
+      if (valid) {
+#pragma unroll 4
+        for (int k = 0; k < D / 8; ++k) {
+          const uint4 v = __ldg(src + k);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+        }
+      }
+      const int sh = min(7 + 127 - static_cast<int>(top >> 7), 120);
+      const float f = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
+      // an infinite or NaN query saturates in e4m3: its scores are NaN instead
+      s_factor[(seg & 1) * kRows + tid] =
+          top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
+                         : a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+      const uint32_t dst = tmem + lanes + kColQ + (seg & 1) * (D / 2);
+#pragma unroll 1
+      for (int k = 0; k < D / 32; ++k) {  // 32 elements: 8 columns of each part
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint4 v = valid ? __ldg(src + 4 * k + e) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t h2[4], l2[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float x = bf_lo(w[j]) * f, y = bf_hi(w[j]) * f;
+            h2[j] = e4m3x2(x, y);
+            const float2 back = floats(halves(h2[j]));
+            l2[j] = e4m3x2(x - back.x, y - back.y);
+          }
+          hi[2 * e] = h2[0] | (h2[1] << 16);
+          hi[2 * e + 1] = h2[2] | (h2[3] << 16);
+          lo[2 * e] = l2[0] | (l2[1] << 16);
+          lo[2 * e + 1] = l2[2] | (l2[3] << 16);
+        }
+        tmem_st<8>(dst + 8 * k, hi);
+        tmem_st<8>(dst + D / 4 + 8 * k, lo);
+      }
+      sm100::tmem_st_wait();
+      sm100::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(&q_full[seg & 1]);
+    };
     int it = 0, seg = 0;
     bool ok = true;
-    Segment g;
-    for (long long u = u0; ok && next_segment(u, g); ++seg) {
-      // the segment before the last has left the queries' columns (its products are
-      // older than tile it - 2's)
-      if (it >= 2 && !wait(&o_done[it & 1], ((it >> 1) - 1) & 1)) {
-        give_up(kFaultSoftmax);
-        break;
-      }
-      {
-        // q 2^sh = hi + lo, its largest magnitude in [128, 256)
-        const int r = g.rt * kRows + row_of_lane<COPIES>(tid);
-        const bool valid = r < g.s.nn * a.G;
-        const int t = valid ? r / a.G : 0;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            a.q + ((static_cast<size_t>(g.b) * a.T + t) * a.Hq + g.h * a.G + (r - t * a.G)) * D);
-        uint32_t w[D / 2];
-        uint32_t top = 0;
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k) {
-          const uint4 v = valid ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
-          w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
-        }
-#pragma unroll
-        for (int k = 0; k < D / 2; ++k) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-        const int sh = min(7 + 127 - static_cast<int>(top >> 7), 120);
-        const float f = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
-        // an infinite or NaN query saturates in e4m3: its scores are NaN instead
-        s_factor[(seg & 1) * kRows + tid] =
-            top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
-                           : a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-        const uint32_t dst = tmem + lanes + kColQ + (seg & 1) * (D / 2);
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k) {  // 64 elements: 16 columns of each part
-          uint32_t hi[16], lo[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            uint32_t h2[2], l2[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t two = w[32 * k + 2 * e + j];
-              const float x = bf_lo(two) * f, y = bf_hi(two) * f;
-              h2[j] = e4m3x2(x, y);
-              const float2 back = floats(halves(h2[j]));
-              l2[j] = e4m3x2(x - back.x, y - back.y);
-            }
-            hi[e] = h2[0] | (h2[1] << 16);
-            lo[e] = l2[0] | (l2[1] << 16);
-          }
-          tmem_st<16>(dst + 16 * k, hi);
-          tmem_st<16>(dst + D / 4 + 16 * k, lo);
-        }
-        sm100::tmem_st_wait();
-        sm100::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) sm100::mbar_arrive(&q_full[seg & 1]);
-      }
+    Segment g, next;
+    long long u = u0;
+    bool more = next_segment(u, next);
+    if (more) stage_queries(next, 0);
+    for (; ok && more; ++seg) {
+      g = next;
+      more = next_segment(u, next);
+      const int before = it - 1;  // last tile of the segment before
       for (int ti = g.t0; ti < g.t1; ++ti, ++it) {
         const int s = it % kStages, k2 = it & 1;
         if (!wait(&full[s], (it / kStages) & 1) ||
@@ -690,6 +701,16 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
         if (lane == 0) {
           sm100::mbar_arrive(&pv_full[k2]);
           sm100::mbar_arrive(&empty[s]);
+        }
+        if (more && ti == min(g.t0 + 1, g.t1 - 1)) {
+          // the next segment's queries go where the one before's were; its products are
+          // done once its last tile's weighted values are
+          if (before >= 0 && !wait(&o_done[before & 1], (before >> 1) & 1)) {
+            give_up(kFaultSoftmax);
+            ok = false;
+            break;
+          }
+          stage_queries(next, seg + 1);
         }
       }
     }
@@ -839,6 +860,17 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
       }
       // ---- the segment's sums ----
       const int last = it - 1;
+      if (g.t0 == 0 && threadIdx.x == 0) {
+        // CTA j begins at unit floor(total j / ctas): inside the item while that is
+        // below its end
+        int n = 0;
+        if (g.end < g.item_end)
+          n = static_cast<int>((g.item_end * s_ctas + s_total - 1) / s_total) -
+              static_cast<int>(blockIdx.x) - 1;
+        const int rts = (a.T * a.G + kRows - 1) / kRows;
+        a.item_ctas[(static_cast<size_t>(g.b) * a.Hkv + g.h) * rts + g.rt] =
+            make_int2(static_cast<int>(blockIdx.x) + 1, n);
+      }
       need(&o_done[last & 1], (last >> 1) & 1);
       sm100::tc_fence_after();
       if (live) {
@@ -1119,29 +1151,17 @@ __global__ void __launch_bounds__(128, 2) finish_kernel(const AttnArgs a) {
   // ---- partial sums over the cached tokens ----
   uno::grid_dependency_wait();
   if (sq.tiles > 0) {
-    const Head hd = *a.head;
     const int rt = r0 / kRows;
-    const long long start = a.base[b] + static_cast<long long>(h * sq.rts + rt) * (sq.tiles + kLead);
-    // CTAs [j0, j1) begin inside the item's tiles
-    int j0 = static_cast<int>(start * hd.ctas / hd.units);
-    while (j0 < hd.ctas && first_unit(hd, j0) <= start + kLead) ++j0;
-    int j1 = j0;
-    while (j1 < hd.ctas && first_unit(hd, j1) < start + kLead + sq.tiles) ++j1;
-    const int n = a.copies * (1 + j1 - j0);
+    const int2 more = a.item_ctas[(static_cast<size_t>(b) * a.Hkv + h) *
+                                      ((a.T * a.G + kRows - 1) / kRows) + rt];
     const int lanes_per_copy = kRows / a.copies;
-    for (int k = kw; k < n; k += KW) {
-      const int cp = k % a.copies, j = k / a.copies;
-      const float2* ml = j == 0 ? a.item_ml : a.cta_ml;
-      const float* po = j == 0 ? a.item_o : a.cta_o;
+    // adds the partial sums at rows at0 + r (r of this lane's rows) of ml and po
+    auto add = [&](const float2* ml, const float* po, size_t at0, int r_off) {
       float f1[2], f2[2];
       const float4* src[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = min(rows[i], R - 1);
-        const size_t at =
-            j == 0 ? ((static_cast<size_t>(b) * a.Hkv + h) * a.copies + cp) *
-                             (static_cast<size_t>(a.T) * a.G) + r
-                   : static_cast<size_t>(j0 + j - 1) * kRows + cp * lanes_per_copy + (r - rt * kRows);
+        const size_t at = at0 + min(rows[i], R - 1) - r_off;
         const float2 v = ml[at];
         src[i] = reinterpret_cast<const float4*>(po + at * D + c * (D / 4));
         const float mx = fmaxf(m[i], v.x);
@@ -1163,7 +1183,15 @@ __global__ void __launch_bounds__(128, 2) finish_kernel(const AttnArgs a) {
             for (int x = 0; x < 4; ++x)
               o[4 * e + x][2 * i + q] = fmaf(w[x], f2[i], o[4 * e + x][2 * i + q] * f1[i]);
           }
-    }
+    };
+    for (int cp = kw; cp < a.copies; cp += KW)
+      add(a.item_ml, a.item_o,
+          ((static_cast<size_t>(b) * a.Hkv + h) * a.copies + cp) * (static_cast<size_t>(a.T) * a.G),
+          0);
+    for (int k = kw; k < a.copies * more.y; k += KW)
+      add(a.cta_ml, a.cta_o,
+          static_cast<size_t>(more.x + k / a.copies) * kRows + k % a.copies * lanes_per_copy,
+          rt * kRows);
   }
   if constexpr (KW > 1) {
     if (kw > 0) {
@@ -1222,7 +1250,7 @@ __global__ void __launch_bounds__(128, 2) finish_kernel(const AttnArgs a) {
 int copies_for(long long rows) { return rows <= 32 ? 4 : rows <= 64 ? 2 : 1; }
 
 struct Layout {
-  size_t base, item_ml, item_o, cta_ml, cta_o, bytes;
+  size_t item_ml, item_o, cta_ml, cta_o, bytes;
 };
 
 Layout layout(int B, int T, int Hq, int Hkv, int D) {
@@ -1231,8 +1259,7 @@ Layout layout(int B, int T, int Hq, int Hkv, int D) {
   const size_t items = static_cast<size_t>(B) * Hkv * rows * copies_for(rows);
   const size_t lanes = static_cast<size_t>(kMaxCtas) * kRows;
   Layout w;
-  w.base = 256;
-  w.item_ml = w.base + up(sizeof(long long) * B);
+  w.item_ml = up(sizeof(int2) * static_cast<size_t>(B) * Hkv * ((rows + kRows - 1) / kRows));
   w.item_o = w.item_ml + up(sizeof(float2) * items);
   w.cta_ml = w.item_o + up(sizeof(float) * items * D);
   w.cta_o = w.cta_ml + up(sizeof(float2) * lanes);
@@ -1391,8 +1418,7 @@ extern "C" int uno_block_attention(const void* q, const void* k_new, const void*
   a.num_pages = num_pages;
   a.scale = scale;
   char* ws = static_cast<char*>(workspace);
-  a.head = reinterpret_cast<Head*>(ws);
-  a.base = reinterpret_cast<long long*>(ws + w.base);
+  a.item_ctas = reinterpret_cast<int2*>(ws);
   a.item_ml = reinterpret_cast<float2*>(ws + w.item_ml);
   a.item_o = reinterpret_cast<float*>(ws + w.item_o);
   a.cta_ml = reinterpret_cast<float2*>(ws + w.cta_ml);
