@@ -63,14 +63,14 @@ constexpr int kProducers = 2;  // TMA warps, alternating tiles
 // two MMA issuers (scores; weighted values): a thread that has issued products
 // waits at its next barrier until they are done, so one issuer would leave the
 // tensor pipe idle between the two.
-__host__ __device__ constexpr int parts(int copies) { return copies == 1 ? 4 : 2; }
+__host__ __device__ constexpr int parts(int copies) { return copies == 1 ? 4 : 1; }
 constexpr int threads(int copies) { return 32 * (4 * parts(copies) + 4 + kProducers + 2); }
 constexpr int kMaxCtas = 148;  // one CTA per SM
 constexpr int kMaxT = 4096;    // new tokens per sequence
 constexpr long long kWaitClocks = 2000000000ll;  // bound of every wait: about a second
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kCachedSeqs = 512;  // sequences whose sizes a CTA keeps in shared memory
-constexpr int kLead = 2;       // units that an item's start counts for, in tiles
+constexpr int kLead = 3;       // units that an item's start counts for, in tiles
 constexpr float kLift = 8.f;   // log2 of how far a weight may pass 1 before its row's ref moves
 // Floor of a row's ref: a tile without a finite score leaves it there.
 constexpr float kLowest = -3.0e38f;
@@ -217,7 +217,8 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
 // on the give-up path too, so none is ever missing).
 template <int PARTS>
 __device__ __forceinline__ void meet(int quarter) {
-  asm volatile("bar.sync %0, %1;" ::"r"(quarter + 1), "n"(32 * PARTS) : "memory");
+  if constexpr (PARTS > 1)
+    asm volatile("bar.sync %0, %1;" ::"r"(quarter + 1), "n"(32 * PARTS) : "memory");
 }
 
 // TMEM loads and stores of N consecutive columns (one lane per thread).
@@ -377,6 +378,7 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
     sm100::fence_mbar_init();
   }
   if (warp == kMmaWarp) sm100::tmem_alloc(tmem_holder, 512);
+  if (warp == kFirstProducer && lane < 2) sm100::tma_prefetch_desc(lane ? &map_v : &map_k);
   uno::grid_dependency_wait();
   // finish_kernel may start: what it reads before its own wait is older than this launch
   uno::launch_dependents();
@@ -487,7 +489,8 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
     if (lane == 0) {
       bool ok = true;
       auto need = [&](uint64_t* bar, uint32_t parity) {
-        if (ok && (s_abort || !wait_one(bar, parity))) {
+        if (phase_done(bar, parity)) return true;
+        if (s_abort || !wait_one(bar, parity)) {
           give_up(kFaultMma);
           ok = false;
         }
@@ -495,9 +498,9 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
       };
       auto scores = [&](int it, int seg) {
         const int s = it % kStages;
+        if (!need(&full[s], (it / kStages) & 1)) return;
         // the tile's columns held the weights of tile it - 2
         if (it >= 2 && !need(&o_done[it & 1], ((it >> 1) - 1) & 1)) return;
-        if (!need(&full[s], (it / kStages) & 1)) return;
         sm100::tc_fence_after();
         const uint64_t kd = key_desc<D>(sm100::smem_addr(smem + s * P::kStage));
         const uint32_t d = tmem + (it & 1) * kTile;
@@ -625,7 +628,7 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
           top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
                          : a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
       const uint32_t dst = tmem + lanes + kColQ + (seg & 1) * (D / 2);
-#pragma unroll 1
+#pragma unroll(COPIES == 1 ? 1 : 4)  // (80 registers hold one block of loads)
       for (int k = 0; k < D / 32; ++k) {  // 32 elements: 8 columns of each part
         uint32_t hi[8], lo[8];
 #pragma unroll
@@ -800,11 +803,13 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
                   if (k * CH + e < left) mx = fmaxf(mx, t);
                 }
               }
-              s_top[part * kRows + tl] = mx;
-              meet<PARTS>(quarter);
+              if constexpr (PARTS > 1) {
+                s_top[part * kRows + tl] = mx;
+                meet<PARTS>(quarter);
 #pragma unroll
-              for (int k = 0; k < PARTS; ++k) mx = fmaxf(mx, s_top[k * kRows + tl]);
-              meet<PARTS>(quarter);  // read before a next move writes
+                for (int k = 0; k < PARTS; ++k) mx = fmaxf(mx, s_top[k * kRows + tl]);
+                meet<PARTS>(quarter);  // read before a next move writes
+              }
               if (ti == g.t0) {
                 ref = mx;
               } else {
@@ -830,21 +835,24 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
             if (left >= HC) pass(std::true_type{});
             else pass(std::false_type{});
             const bool ask = !move && __any_sync(0xFFFFFFFFu, top > kLift);
-            if (lane == 0) s_flag[(k2 * 4 + quarter) * 4 + part] = ask;
+            if (PARTS > 1 && lane == 0) s_flag[(k2 * 4 + quarter) * 4 + part] = ask;
             meet<PARTS>(quarter);  // all parts have read the scores that the weights overwrite
             if (move) break;
+            if constexpr (PARTS > 1) {
 #pragma unroll
-            for (int k = 0; k < PARTS; ++k) move |= s_flag[(k2 * 4 + quarter) * 4 + k] != 0;
+              for (int k = 0; k < PARTS; ++k) move |= s_flag[(k2 * 4 + quarter) * 4 + k] != 0;
+            } else {
+              move = ask;
+            }
             if (!move) break;
           }
           l += add;
           tmem_st<HC / 2>(st + c0 / 2, pk);
           if constexpr (COPIES > 1) {
-            // the other copies' tokens get weight 0: 16-column blocks, the parts
-            // taking every other one
+            // the other copies' tokens get weight 0
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if ((k & 1) == part && k / (4 / COPIES) != copy) {
+              if (k / (4 / COPIES) != copy) {
                 const uint32_t z[16] = {};
                 tmem_st<16>(st + 16 * k, z);
               }
@@ -879,8 +887,10 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
                                 (static_cast<size_t>(a.T) * a.G) + r
                       : static_cast<size_t>(blockIdx.x) * kRows + tl;
         float* dst = (g.t0 == 0 ? a.item_o : a.cta_o) + row * D;
-        s_top[part * kRows + tl] = l;
-        meet<PARTS>(quarter);
+        if constexpr (PARTS > 1) {
+          s_top[part * kRows + tl] = l;
+          meet<PARTS>(quarter);
+        }
         if (part == 0 && valid) {
 #pragma unroll
           for (int k = 1; k < PARTS; ++k) l += s_top[k * kRows + tl];
