@@ -59,12 +59,15 @@ constexpr int kRows = 128;     // rows (TMEM lanes) of a tile
 constexpr int kStages = 4;     // tiles of codes in shared memory
 constexpr int kProducers = 2;  // TMA warps, alternating tiles
 // Warps of cached_kernel: 4 parts() for the softmax (TMEM lane quarter = warp % 4, part
-// of a row's tokens = warp / 4), 4 for queries and value decode, the producers, and
-// two MMA issuers (scores; weighted values): a thread that has issued products
+// of a row's tokens = warp / 4), decoders() for the value decode (the first four of them
+// for the queries too), the producers, and two MMA issuers (scores; weighted values): a thread that has issued products
 // waits at its next barrier until they are done, so one issuer would leave the
 // tensor pipe idle between the two.
 __host__ __device__ constexpr int parts(int copies) { return copies == 1 ? 4 : 1; }
-constexpr int threads(int copies) { return 32 * (4 * parts(copies) + 4 + kProducers + 2); }
+__host__ __device__ constexpr int decoders(int copies) { return copies == 1 ? 4 : 8; }
+constexpr int threads(int copies) {
+  return 32 * (4 * parts(copies) + decoders(copies) + kProducers + 2);
+}
 constexpr int kMaxCtas = 148;  // one CTA per SM
 constexpr int kMaxT = 4096;    // new tokens per sequence
 constexpr long long kWaitClocks = 2000000000ll;  // bound of every wait: about a second
@@ -332,7 +335,8 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
   constexpr int CW = kTile / COPIES;  // a row copy's tokens per tile
   constexpr int PARTS = parts(COPIES);
   constexpr int HC = CW / PARTS;      // a softmax thread's
-  constexpr int kFirstDecode = 4 * PARTS, kFirstProducer = kFirstDecode + 4;
+  constexpr int DECODERS = decoders(COPIES);
+  constexpr int kFirstDecode = 4 * PARTS, kFirstProducer = kFirstDecode + DECODERS;
   constexpr int kMmaWarp = kFirstProducer + kProducers;  // scores (and TMEM); + 1: values
   // TMEM columns: two score tiles (their weights over them), o, the queries' parts
   // of two segments
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
   float4* s_scale = reinterpret_cast<float4*>(smem + P::kScales);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + P::kBars);  // codes and scales are there
   uint64_t* empty = full + kStages;   // nobody needs them any more
-  uint64_t* s_full = empty + kStages; // [2] scores and scales of a tile
+  uint64_t* s_full = empty + kStages; // [2] scores of a tile
   uint64_t* pv_full = s_full + 2;     // [2] weights and decoded values of a tile
   uint64_t* o_done = pv_full + 2;     // [2] a tile's weighted values are in o
   uint64_t* q_full = o_done + 2;      // [2] a segment's queries
@@ -365,11 +369,11 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       sm100::mbar_init(&full[s], 1);
-      sm100::mbar_init(&empty[s], 4 * PARTS + 5);  // softmax and decode warps, a commit
+      sm100::mbar_init(&empty[s], 4 * PARTS + DECODERS + 1);  // softmax and decode warps, a commit
     }
     for (int k = 0; k < 2; ++k) {
-      sm100::mbar_init(&s_full[k], 5);  // the issuer's commit, decode warps
-      sm100::mbar_init(&pv_full[k], 4 * PARTS + 4);  // softmax and decode warps
+      sm100::mbar_init(&s_full[k], 1);
+      sm100::mbar_init(&pv_full[k], 4 * PARTS + DECODERS);  // softmax and decode warps
       sm100::mbar_init(&o_done[k], 1);
       sm100::mbar_init(&q_full[k], 4);
     }
@@ -603,8 +607,9 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
     // ---- queries of a segment to e4m3 parts, codes of a tile's values to halves ----
     const int tid = threadIdx.x - 32 * kFirstDecode;
     const uint32_t lanes = static_cast<uint32_t>(tid & 96) << 16;
-    // The queries of segment `seg`, in the columns that those of segment seg - 2 have left.
+    // (the first four warps) The queries of segment `seg`, in the columns that those of segment seg - 2 have left.
     auto stage_queries = [&](const Segment& g, int seg) {
+      if (tid >= 128) return;
       // q 2^sh = hi + lo, its largest magnitude in [128, 256)
       const int r = g.rt * kRows + row_of_lane<COPIES>(tid);
       const bool valid = r < g.s.nn * a.G;
@@ -674,16 +679,14 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
           ok = false;
           break;
         }
-        // the scales that full[s] came with are the softmax warps' to read, too
-        if (lane == 0) sm100::mbar_arrive(&s_full[k2]);
         const uint8_t* src = smem + s * P::kStage + kTile * D;
         uint8_t* dst = smem + P::kDecoded + k2 * P::kHalfTile;
         const int left = g.s.len - ti * kTile;
         constexpr int kPieces = D / 16;  // 16-byte pieces of a token
         const int ch = tid % kPieces;
 #pragma unroll
-        for (int st = 0; st < kTile * kPieces / 128; ++st) {
-          const int t = tid / kPieces + st * (128 / kPieces);
+        for (int st = 0; st < kTile * kPieces / (32 * DECODERS); ++st) {
+          const int t = tid / kPieces + st * (32 * DECODERS / kPieces);
           const int sw = D == 128 ? (t & 7) : ((t >> 1) & 3);
           uint4 w = *reinterpret_cast<const uint4*>(src + t * D + ((ch ^ sw) << 4));
           // slots behind the sequence may hold anything, NaN too
@@ -705,7 +708,7 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
           sm100::mbar_arrive(&pv_full[k2]);
           sm100::mbar_arrive(&empty[s]);
         }
-        if (more && ti == min(g.t0 + 1, g.t1 - 1)) {
+        if (more && tid < 128 && ti == min(g.t0 + 1, g.t1 - 1)) {
           // the next segment's queries go where the one before's were; its products are
           // done once its last tile's weighted values are
           if (before >= 0 && !wait(&o_done[before & 1], (before >> 1) & 1)) {
@@ -744,6 +747,7 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
       float ref = kLowest, l = 0.f;
       for (int ti = g.t0; ti < g.t1; ++ti, ++it) {
         const int s = it % kStages, k2 = it & 1;
+        need(&full[s], (it / kStages) & 1);  // the scales
         need(&s_full[k2], (it >> 1) & 1);
         sm100::tc_fence_after();
         const uint32_t st = tmem + lanes + k2 * kTile;
