@@ -47,7 +47,8 @@ def _check_cuda(*ts: Optional[torch.Tensor]) -> torch.device:
 
 
 def _stream_handle(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    # the raw handle of torch.cuda.current_stream(device), without its Stream object (2 us a call)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 class _Workspaces:
@@ -587,8 +588,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, *,
     with _on(dev):
         h = x if residual is None else torch.empty_like(x)
         y = torch.empty_like(x) if want_y else None
-        q = torch.empty((M, d), dtype=torch.int8, device=dev) if want_q else None
-        scale = torch.empty((M,), dtype=torch.float32, device=dev) if want_q else None
+        q = torch.empty_like(x, dtype=torch.int8) if want_q else None
+        scale = x.new_empty(M, dtype=torch.float32) if want_q else None
         st = lib.uno_rms_norm(_ptr(x), _ptr(residual), _ptr(weight), float(eps), M, d, dt,
                               None if residual is None else _ptr(h), _ptr(y), _ptr(q),
                               _ptr(scale), _stream_handle(dev))
@@ -608,8 +609,8 @@ def quantize_rows(x: torch.Tensor):
     dt = _dtype_code(x)
     dev = _check_cuda(x)
     with _on(dev):
-        q = torch.empty((M, d), dtype=torch.int8, device=dev)
-        scale = torch.empty((M,), dtype=torch.float32, device=dev)
+        q = torch.empty_like(x, dtype=torch.int8)
+        scale = x.new_empty(M, dtype=torch.float32)
         st = lib.uno_quantize_rows(_ptr(x), M, d, dt, _ptr(q), _ptr(scale), _stream_handle(dev))
     if st != 0:
         raise UnoError(st, "uno_quantize_rows")
@@ -661,13 +662,13 @@ def dualpath_linear_int8(xq: torch.Tensor, x_scale: torch.Tensor, Wq: torch.Tens
             raise ValueError("adapter rank must be at least 8")
     dev = _check_cuda(xq, x_scale, Wq, w_scale, Aq, a_scale, Bm, workspace)
     with _on(dev):
-        y_ar = torch.empty((M, d_out), dtype=out_dtype, device=dev) if want_ar else None
-        y_draft = torch.empty((M, d_out), dtype=out_dtype, device=dev) if adapter else None
+        y_ar = xq.new_empty((M, d_out), dtype=out_dtype) if want_ar else None
+        y_draft = xq.new_empty((M, d_out), dtype=out_dtype) if adapter else None
         if workspace is None:
             # one of its own per call: calls on other streams, or replays of
             # captured ones, never meet in it
             need = int(lib.uno_dualpath_int8_workspace_bytes(M, d_in, d_out, r))
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = xq.new_empty(need, dtype=torch.uint8)
         st = lib.uno_dualpath_linear_int8(
             _ptr(xq), _ptr(x_scale), _ptr(Wq), _ptr(w_scale), _ptr(Aq), _ptr(a_scale), _ptr(Bm),
             float(scale), _gate_arg(gate, M, dev), _ptr(y_ar), _ptr(y_draft), M, d_in, d_out, r,
@@ -786,7 +787,7 @@ def block_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, c
             out = torch.empty_like(q) if num_new is None else torch.zeros_like(q)
         if workspace is None:  # one of its own per call, as for dualpath_linear_int8
             need = int(lib.uno_block_attention_workspace_bytes(B, T, Hq, Hkv, D))
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = q.new_empty(need, dtype=torch.uint8)
         st = lib.uno_block_attention(
             _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(lens), _ptr(parent), _ptr(num_new),
             D ** -0.5 if scale is None else float(scale), B, T, Hq, Hkv, D, cache.k.shape[2],
