@@ -191,15 +191,23 @@ __host__ __device__ constexpr int swap_stat_bytes() {
   return PAIR ? 0 : 4 * 2 * BN * 8 + 4 * 32 * 33 * 4;  // + the warps' transpose scratch
 }
 
-template <int BN, bool PAIR>
+// int8 operands with bf16 outputs in the pair layout: every epilogue warp stages
+// its 32 rows' stores, two boxes of 64 columns, behind the ring.
+template <typename T, typename Y, bool PAIR>
+__host__ __device__ constexpr int store_stage_bytes() {
+  return PAIR && sizeof(T) == 1 && sizeof(Y) == 2 ? 4 * 2 * 4096 : 0;
+}
+
+template <int BN, bool PAIR, typename T = uint16_t, typename Y = T>
 __host__ __device__ constexpr int smem_bytes() {
   static_assert(barrier_bytes<BN, PAIR>() <= 256, "barrier region");
   return stages_for<BN, PAIR>() * stage_bytes<BN, PAIR>() + 1024 /*align*/ + 256 /*barriers*/ +
-         swap_stat_bytes<BN, PAIR>();
+         swap_stat_bytes<BN, PAIR>() + store_stage_bytes<T, Y, PAIR>();
 }
 static_assert(smem_bytes<256, false>() <= 232448 && smem_bytes<128, false>() <= 232448 &&
                   smem_bytes<64, false>() <= 232448 && smem_bytes<32, false>() <= 232448 &&
-                  smem_bytes<256, true>() <= 232448,
+                  smem_bytes<256, true>() <= 232448 &&
+                  smem_bytes<256, true, int8_t, uint16_t>() <= 232448,
               "dynamic shared memory per CTA (227 KB)");
 
 __device__ __forceinline__ void set_fault(unsigned bit, volatile int* abort_flag) {
@@ -483,7 +491,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + STAGES * kStage);
+  constexpr int kStoreStage = store_stage_bytes<T, Y, PAIR>();  // behind the ring (1024-aligned)
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + STAGES * kStage + kStoreStage);
   uint64_t* empty_bar = full_bar + STAGES;
   uint64_t* acc_full = empty_bar + STAGES;  // [2] main product done
   uint64_t* ar_read = acc_full + 2;         // [2] epilogue drained y_ar
@@ -494,7 +503,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 2);
   int* order = reinterpret_cast<int*>(tmem_holder + 1);  // next ring item to issue
   // swapped layout with row statistics: [4 epilogue warps][2 outputs][BN] (m, z)
-  float2* srs = reinterpret_cast<float2*>(smem + STAGES * kStage + 256);
+  float2* srs = reinterpret_cast<float2*>(smem + STAGES * kStage + kStoreStage + 256);
   const bool swap_stats = SWAP && (p.g[0].stats_ar != nullptr || p.g[0].stats_draft != nullptr);
   __shared__ volatile int abort_flag;
 
@@ -1058,6 +1067,69 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           stats[static_cast<size_t>(arow) * stats_tiles + b0 / BN] = make_float2(rs.m, rs.z);
       }
     };
+    // int8 with bf16 outputs in the pair layout: as drain, but through TMA stores of
+    // 64-column boxes from the warp's two staging boxes. Lanes hold rows, so direct
+    // stores write 16-byte pieces of 32 rows at a time, and with the products twice as
+    // fast as bf16's the epilogue sets the pace (1088 x 4096 -> 12288, both paths:
+    // 94 us with direct stores).
+    auto drain_tma = [&](uint32_t acc, int a0, int b0, const CUtensorMap* map, bool store,
+                         bool from_f32, bool keep) {
+      const uint32_t tq = acc + (static_cast<uint32_t>(quarter * 32) << 16);
+      uint8_t* stage = smem + STAGES * kStage + quarter * 8192;
+      const uint32_t sw = static_cast<uint32_t>(lane & 7);
+      const float sa = from_f32 ? 1.f : side_a(a0 + lane);
+#pragma unroll 1
+      for (int box = 0; box < BN / 64; ++box) {
+        uint8_t* dst = stage + (box & 1) * 4096 + lane * 128;
+        if (store && box >= 2) {
+          // this box's last store has read it
+          if (lane == 0)
+            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          __syncwarp();
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = box * 64 + h * 32;
+          uint32_t v[32];
+          sm100::tmem_ld_32x32b_x32(tq + c, v);
+          sm100::tmem_ld_wait();
+          float f[32];
+          if (from_f32) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]);
+          } else {
+            scaled(v, f, sa, p.g[gi].w_scale, b0 + c, ncols);
+            if (keep) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(f[e]);
+              sm100::tmem_st_32x32b_x32(tq + c, v);
+            }
+          }
+          if (store) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              *reinterpret_cast<uint4*>(dst + (((h * 4 + g) ^ sw) << 4)) =
+                  make_uint4(pack_bf16x2(f[8 * g], f[8 * g + 1]),
+                             pack_bf16x2(f[8 * g + 2], f[8 * g + 3]),
+                             pack_bf16x2(f[8 * g + 4], f[8 * g + 5]),
+                             pack_bf16x2(f[8 * g + 6], f[8 * g + 7]));
+          }
+        }
+        if (store) {
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            sm100::tma_store_2d(map, stage + (box & 1) * 4096, b0 + 64 * box, a0);
+            sm100::bulk_commit_group();
+          }
+        }
+      }
+      if (keep) sm100::tmem_st_wait();
+      if (store) {  // the next drain begins with both boxes free
+        if (lane == 0) sm100::bulk_wait_group_read_0();
+        __syncwarp();
+      }
+    };
     // Drain y_ar = acc and y_draft = acc + adp (both BN columns wide).
     // Last tile with bf16 outputs and the pair layout: the ring is idle by
     // now, so each warp stages its 32 rows of y_ar and y_draft in shared
@@ -1358,9 +1430,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         break;
       }
-      drain(acc, x.a0 + my_rows, x.b0, ya, ncols, p.M, BN, 1.f, nullptr, p.g[gi].stats_ar,
-            p.g[gi].stats_tiles, 0, !kI8, side_a(x.a0 + my_rows + rr),
-            SWAP ? p.x_scale : p.g[gi].w_scale, SWAP ? p.M : ncols, kI8 && adapter);
+      if (kStoreStage > 0 && whole && (ya || adapter))
+        drain_tma(acc, x.a0 + my_rows + quarter * 32, x.b0, &m.ya[gi], ya != nullptr, false,
+                  adapter);
+      else
+        drain(acc, x.a0 + my_rows, x.b0, ya, ncols, p.M, BN, 1.f, nullptr, p.g[gi].stats_ar,
+              p.g[gi].stats_tiles, 0, !kI8, side_a(x.a0 + my_rows + rr),
+              SWAP ? p.x_scale : p.g[gi].w_scale, SWAP ? p.M : ncols, kI8 && adapter);
       sm100::tc_fence_before();
       __syncwarp();
       const int mo = li - nt_mine;
@@ -1372,8 +1448,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         break;
       }
       sm100::tc_fence_after();
-      drain(acc, x.a0 + my_rows, x.b0, yd, ncols, p.M, BN, 1.f, nullptr, p.g[gi].stats_draft,
-            p.g[gi].stats_tiles, 1);
+      if (kStoreStage > 0 && whole)
+        drain_tma(acc, x.a0 + my_rows + quarter * 32, x.b0, &m.yd[gi], true, true, false);
+      else
+        drain(acc, x.a0 + my_rows, x.b0, yd, ncols, p.M, BN, 1.f, nullptr, p.g[gi].stats_draft,
+              p.g[gi].stats_tiles, 1);
       sm100::tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_leader(&acc_empty[buf]);
@@ -1542,7 +1621,7 @@ int max_pairs(K kern, int bytes) {
 
 template <typename T, typename Y, int BN, bool SWAP, bool PAIR>
 int launch_dual(const DualMaps& maps, const GemmParams& p, cudaStream_t st) {
-  constexpr int bytes = smem_bytes<BN, PAIR>();
+  constexpr int bytes = smem_bytes<BN, PAIR, T, Y>();
   auto kern = dual_kernel<T, Y, BN, SWAP, PAIR>;
   static std::atomic<uint64_t> attr_done{0};  // devices with the shared-memory opt-in
   int dev = 0;
@@ -1569,8 +1648,10 @@ int launch_dual(const DualMaps& maps, const GemmParams& p, cudaStream_t st) {
   q.split_start = static_cast<int>(units0);
   q.split_k = 1;
   long long tiles = units0;
-  if (units0 > resident) {
-    const long long rem = units0 % resident;
+  // (int8: also when all tiles together would leave most SMs idle; its sums are exact,
+  // so the pieces change no result)
+  if (units0 > resident || (sizeof(T) == 1 && 3 * units0 <= resident)) {
+    const long long rem = units0 > resident ? units0 % resident : p.main_tiles;
     int k = rem > 0 ? static_cast<int>(std::min<long long>(kMaxSplit, resident / rem)) : 1;
     while (k > 1 && p.kb_total < 2 * k) --k;
     const size_t per_slot = static_cast<size_t>(PAIR ? 2 : 1) * kBM * BN * sizeof(float);
@@ -1751,8 +1832,8 @@ int run_dualpath(int n, const void* x, const void* const* W, const void* const* 
              make_map(&maps.t[g], a.t_buf, t_dtype, r, M, kBM) &&
              make_map(&maps.l[g], A[g], dtype, d_in, r, n_t / 2);
       // output maps of the TMA-store epilogue (bf16): 32 rows x 64 columns
-      if (ok && adapter && sizeof(Y) == 2 && d_out[g] % 8 == 0) {
-        ok = make_store_map(&maps.yd[g], y_draft[g], d_out[g], M);
+      if (ok && (adapter || i8) && sizeof(Y) == 2 && d_out[g] % 8 == 0) {
+        if (adapter) ok = make_store_map(&maps.yd[g], y_draft[g], d_out[g], M);
         if (ok && y_ar[g]) ok = make_store_map(&maps.ya[g], y_ar[g], d_out[g], M);
       }
     }

@@ -59,7 +59,7 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
   return f;
 }
 
-__global__ void kv_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
   __shared__ uint32_t s_max[32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = static_cast<int>(blockIdx.x) / a.pages_per_seq;
@@ -78,29 +78,53 @@ __global__ void kv_append_kernel(const AppendArgs a) {
   const int id = a.table[static_cast<size_t>(b) * a.width + page_no];
   if (id < 0 || id >= a.num_pages) return;
   const int slot0 = start + t0 - page_no * a.page;
-  const int vecs = a.D / 8;  // 16-byte pieces of a row
-  const int total = (t1 - t0) * vecs;
+  // 16-byte pieces: 2^lv of a row; a thread's pieces are `step` rows apart
+  const int lv = a.D == 128 ? 4 : 3;
+  const int step = static_cast<int>(blockDim.x) >> lv;
+  const int first = tid >> lv, d = (tid - (first << lv)) * 8;
+  const size_t stride = static_cast<size_t>(a.Hkv) * a.D;  // from token to token
+  const uint16_t* x = a.x[kv] + static_cast<size_t>(b) * a.T * stride + head * a.D + d;
   uint4 v[kPieces];
   uint32_t top = 0;
+  const int n = t1 - t0 - first;  // tokens from this thread's first one on
+  if (a.rows) {
+    const int32_t* rows = a.rows + static_cast<size_t>(b) * a.n + t0 + first;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int row = i * step < n ? rows[i * step] : 0;
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (i * step < n)
+        v[i] = row < 0 || row >= a.T
+                   ? make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u)
+                   : *reinterpret_cast<const uint4*>(x + row * stride);
+    }
+  } else {
+    const uint16_t* src = x + (t0 + first) * stride;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (i * step < n) v[i] = *reinterpret_cast<const uint4*>(src + i * step * stride);
+    }
+  }
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
-    const int p = tid + i * static_cast<int>(blockDim.x);
-    v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (p < total) {
-      const int t = t0 + p / vecs, d = (p % vecs) * 8;
-      const int row = a.rows ? a.rows[static_cast<size_t>(b) * a.n + t] : t;
-      if (row < 0 || row >= a.T)
-        v[i] = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
-      else
-        v[i] = *reinterpret_cast<const uint4*>(
-            a.x[kv] + ((static_cast<size_t>(b) * a.T + row) * a.Hkv + head) * a.D + d);
-    }
     const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {  // bf16 magnitudes order like their bits; non-finite ones drop out
-      const uint32_t lo = w[k] & 0x7FFFu, hi = (w[k] >> 16) & 0x7FFFu;
-      if (lo < 0x7F80u) top = max(top, lo);
-      if (hi < 0x7F80u) top = max(top, hi);
+    for (int k = 0; k < 4; ++k)  // bf16 magnitudes order like their bits
+      top = __vmaxu2(top, w[k] & 0x7FFF7FFFu);
+  }
+  top = max(top & 0xFFFFu, top >> 16);
+  if (top >= 0x7F80u) {  // infinities and NaN drop out
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = w[k] & 0x7FFFu, hi = (w[k] >> 16) & 0x7FFFu;
+        if (lo < 0x7F80u) top = max(top, lo);
+        if (hi < 0x7F80u) top = max(top, hi);
+      }
     }
   }
   top = __reduce_max_sync(0xFFFFFFFFu, top);
@@ -120,7 +144,7 @@ __global__ void kv_append_kernel(const AppendArgs a) {
   if (now > old) {  // the page's earlier tokens move to the larger scale
     const float grow = old / now;
     uint2* c = reinterpret_cast<uint2*>(codes);
-    for (int p = tid; p < slot0 * vecs; p += static_cast<int>(blockDim.x)) {
+    for (int p = tid; p < slot0 << lv; p += static_cast<int>(blockDim.x)) {
       const uint2 w = c[p];
       uint32_t o[2];
       const uint32_t in[2] = {w.x, w.y};
@@ -132,15 +156,15 @@ __global__ void kv_append_kernel(const AppendArgs a) {
       c[p] = make_uint2(o[0], o[1]);
     }
   }
+  uint8_t* dst = codes + (slot0 + first) * a.D + d;
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
-    const int p = tid + i * static_cast<int>(blockDim.x);
-    if (p < total) {
+    if (i * step < n) {
       float f[8];
       uno::LogitRow<uint16_t>::unpack(v[i], f);
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[k] *= inv;
-      *reinterpret_cast<uint2*>(codes + static_cast<size_t>(slot0) * a.D + p * 8) =
+      *reinterpret_cast<uint2*>(dst + i * step * a.D) =
           make_uint2(e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16),
                      e4m3x2(f[4], f[5]) | (e4m3x2(f[6], f[7]) << 16));
     }

@@ -5,15 +5,18 @@
 //   y = h * rsqrt(mean(h^2) + eps) * w
 //   scale = max|y| / 127, q = rint(y / scale)
 //
-// Bound by HBM: x (and the residual) come in once, h and q go out once, so
-// a row stays in registers between its loads and its stores. The row factor
+// Bound by HBM, and at 2 bytes in and 1 out nearly by issue slots: x (and the
+// residual) come in once, h and q go out once, a row stays in registers between
+// its loads and its stores, and an element costs few instructions (a rounding is
+// one fma onto 1.5 * 2^23, whose low byte is then the integer: 82 us against
+// 139 us of 8192 x 12288 with conversions to int). The row factor
 // r = rsqrt(..) scales every |h w| alike, so max|y| = r max|h w| and
 // q = rint(h w * 127 / max|h w|): the sum of squares and the maximum are one
 // block reduction, not two with the row read again between them.
 //
-// Maxima are taken over the bit patterns of |v| (ordered like the values,
-// with infinities and NaN above every finite number), so that a non-finite row
-// is seen: it stores scale = NaN and q = 0.
+// Maxima keep NaN and are compared as bit patterns across threads (NaN above
+// infinity above every finite number), so that a non-finite row is seen: it
+// stores scale = NaN and q = 0.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -89,8 +92,16 @@ __device__ __forceinline__ void store_v(T* p, const float* f) {
   }
 }
 
+// max(m, |v|) that keeps a NaN of either.
+__device__ __forceinline__ float max_abs(float m, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  return r;
+}
+
+// The integers in the low bytes of V words to memory.
 template <int V>
-__device__ __forceinline__ void store_q(int8_t* p, const int* q) {
+__device__ __forceinline__ void store_q(int8_t* p, const uint32_t* q) {
   if constexpr (V == 1) {
     *p = static_cast<int8_t>(q[0]);
   } else {
@@ -100,6 +111,23 @@ __device__ __forceinline__ void store_q(int8_t* p, const int* q) {
       w[k] = __byte_perm(__byte_perm(q[4 * k], q[4 * k + 1], 0x0040),
                          __byte_perm(q[4 * k + 2], q[4 * k + 3], 0x0040), 0x5410);
     *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  }
+}
+
+// f + r in the rows' type: written to h (where given) and read back from it.
+template <typename T, int V>
+__device__ __forceinline__ void add_rows(float* f, const float* r, T* h) {
+#pragma unroll
+  for (int k = 0; k < V; ++k) f[k] += r[k];
+  if constexpr (V == 8 && sizeof(T) == 2) {
+    const uint4 w = make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]),
+                               bf16x2(f[6], f[7]));
+    uno::LogitRow<T>::unpack(w, f);
+    if (h) *reinterpret_cast<uint4*>(h) = w;
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) f[k] = to_f32<T>(from_f32<T>(f[k]));
+    if (h) store_v<T, V>(h, f);
   }
 }
 
@@ -132,23 +160,23 @@ __global__ void __launch_bounds__(1024) row_quant_kernel(const RowArgs a, int wa
     for (int k = 0; k < V; ++k) f[i][k] = 0.f;
     if (in[i]) load_v<T, V>(x + e, f[i]);
   }
-  if (res) {
+  if (NORM) {
+    T* h = static_cast<T*>(a.h);
+    if (res) {
+      float r[ITER][V];
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-      if (!in[i]) continue;
-      float r[V];
-      load_v<T, V>(res + tid * V + i * step, r);
+      for (int i = 0; i < ITER; ++i)
+        if (in[i]) load_v<T, V>(res + tid * V + i * step, r[i]);
 #pragma unroll
-      for (int k = 0; k < V; ++k) f[i][k] = to_f32<T>(from_f32<T>(f[i][k] + r[k]));
+      for (int i = 0; i < ITER; ++i)
+        if (in[i]) add_rows<T, V>(f[i], r[i], h ? h + at + tid * V + i * step : nullptr);
+    } else if (h) {
+#pragma unroll
+      for (int i = 0; i < ITER; ++i)
+        if (in[i]) store_v<T, V>(h + at + tid * V + i * step, f[i]);
     }
   }
-  if (NORM && a.h) {
-#pragma unroll
-    for (int i = 0; i < ITER; ++i)
-      if (in[i]) store_v<T, V>(static_cast<T*>(a.h) + at + tid * V + i * step, f[i]);
-  }
-  float sum = 0.f;
-  uint32_t top = 0;
+  float sum = 0.f, big = 0.f;
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
     if (NORM) {
@@ -162,8 +190,9 @@ __global__ void __launch_bounds__(1024) row_quant_kernel(const RowArgs a, int wa
       }
     }
 #pragma unroll
-    for (int k = 0; k < V; ++k) top = max(top, __float_as_uint(f[i][k]) & 0x7FFFFFFFu);
+    for (int k = 0; k < V; ++k) big = max_abs(big, f[i][k]);
   }
+  uint32_t top = __float_as_uint(big);
   top = __reduce_max_sync(0xFFFFFFFFu, top);
   if (NORM) {
 #pragma unroll
@@ -197,18 +226,33 @@ __global__ void __launch_bounds__(1024) row_quant_kernel(const RowArgs a, int wa
   const float amax = __uint_as_float(top);
   const bool bad = top >= 0x7F800000u || !(sum < INFINITY);
   const float inv = bad ? 0.f : 127.f / amax;
-  const bool plain = inv < INFINITY;  // amax = 0 and amax below 127 / FLT_MAX divide instead
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: an integer added to it stays in the low bits
+  int8_t* dst = a.q + at + tid * V;
+  if (inv < INFINITY) {
 #pragma unroll
-  for (int i = 0; i < ITER; ++i) {
-    if (!in[i]) continue;
-    int q[V];
+    for (int i = 0; i < ITER; ++i) {
+      if (!in[i]) continue;
+      uint32_t q[V];
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      float v = 0.f;
-      if (!bad && amax > 0.f) v = plain ? f[i][k] * inv : f[i][k] / amax * 127.f;
-      q[k] = __float2int_rn(v);
+      for (int k = 0; k < V; ++k)
+        q[k] = bad ? 0u : __float_as_uint(fmaf(f[i][k], inv, kRound));
+      store_q<V>(dst + i * step, q);
     }
-    store_q<V>(a.q + at + tid * V + i * step, q);
+  } else {  // amax = 0, or below 127 / FLT_MAX: divide instead
+#pragma unroll 1
+    for (int i = 0; i < ITER; ++i) {
+      if (tid * V + i * step >= a.d) break;
+      uint32_t q[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        float v = 0.f;
+#pragma unroll
+        for (int j = 0; j < ITER; ++j)
+          if (j == i) v = f[j][k];
+        q[k] = __float_as_uint((amax > 0.f ? v / amax * 127.f : 0.f) + kRound);
+      }
+      store_q<V>(dst + i * step, q);
+    }
   }
   if (tid == 0) a.scale[row] = bad ? __uint_as_float(0x7FC00000u) : amax * rstd / 127.f;
 }
@@ -232,6 +276,80 @@ int launch(const RowArgs& a, int warps, cudaStream_t st) {
   return UNO_OK;
 }
 
+// uno_quantize_rows of bfloat16 rows in 16-byte pieces: the row stays packed in
+// registers (half of what its float32 values would take, so that twice the rows
+// are in flight), its maximum is taken two at a time over the bit patterns.
+template <int ITER, int THREADS>
+__global__ void __launch_bounds__(THREADS, 2048 / THREADS) quant_bf16_kernel(const RowArgs a) {
+  __shared__ uint32_t s_max[THREADS / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int step = static_cast<int>(blockDim.x) * 8;
+  uno::launch_dependents();
+  uno::grid_dependency_wait();
+  const size_t at = static_cast<size_t>(blockIdx.x) * a.d + tid * 8;
+  const uint16_t* x = static_cast<const uint16_t*>(a.x) + at;
+  uint4 v[ITER];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid * 8 + i * step < a.d) v[i] = *reinterpret_cast<const uint4*>(x + i * step);
+  }
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w[k] & 0x7FFF7FFFu);
+  }
+  top = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16));
+  if (lane == 0) s_max[warp] = top;
+  __syncthreads();
+  top = __reduce_max_sync(0xFFFFFFFFu,
+                          lane < static_cast<int>(blockDim.x) / 32 ? s_max[lane] : 0u);
+  const float amax = uno::bf16_bits_to_float(top);
+  const bool bad = top >= 0x7F80u;
+  // (bfloat16's smallest magnitudes divide: 127 / amax passes float32)
+  const bool tiny = top < 0x0200u;
+  const float inv = bad || top == 0 ? 0.f : tiny ? 127.f / (amax * 0x1p64f) : 127.f / amax;
+  const float lift = tiny ? 0x1p64f : 1.f;
+  constexpr float kRound = 12582912.f;
+  int8_t* dst = a.q + at;
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    if (tid * 8 + i * step >= a.d) continue;
+    float f[8];
+    uno::LogitRow<uint16_t>::unpack(v[i], f);
+    uint32_t q[8];
+    if (tiny) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] *= lift;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      q[k] = bad ? 0u : __float_as_uint(fmaf(f[k], inv, kRound));
+    store_q<8>(dst + i * step, q);
+  }
+  if (tid == 0) a.scale[blockIdx.x] = bad ? __uint_as_float(0x7FC00000u) : amax / 127.f;
+}
+
+template <int ITER, int THREADS>
+int launch_quant_bf16(const RowArgs& a, int warps, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.M));
+  cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, quant_bf16_kernel<ITER, THREADS>, a) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return UNO_ERR_CUDA;
+  }
+  return UNO_OK;
+}
+
 template <typename T, bool NORM>
 int run(const RowArgs& a, cudaStream_t st) {
   // 16-byte pieces when every row starts on a 16-byte boundary; any other
@@ -239,10 +357,14 @@ int run(const RowArgs& a, cudaStream_t st) {
   if (a.d % 8 == 0) {
     const int pieces = a.d / 8;
     // Few rows: one piece per thread, so that a row's latency is one round of
-    // loads. Many rows: two per thread, four past 1024 threads.
+    // loads. Many rows: four, so that more rows are in flight on an SM.
     if (pieces <= 32 || (pieces <= 1024 && a.M <= 296))
       return launch<T, 8, 1, NORM>(a, (pieces + 31) / 32, st);
-    if (pieces <= 2048) return launch<T, 8, 2, NORM>(a, (pieces + 63) / 64, st);
+    if constexpr (sizeof(T) == 2 && !NORM) {
+      if (pieces <= 2048) return launch_quant_bf16<4, 512>(a, (pieces + 127) / 128, st);
+    }
+    // (float32's would not fit 64 registers; with more, fewer rows are in flight)
+    if (sizeof(T) == 4 && pieces <= 2048) return launch<T, 8, 2, NORM>(a, (pieces + 63) / 64, st);
     return launch<T, 8, 4, NORM>(a, (pieces + 127) / 128, st);
   }
   if (a.d <= 8192) return launch<T, 1, 8, NORM>(a, (a.d + 255) / 256, st);

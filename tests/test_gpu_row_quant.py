@@ -144,3 +144,26 @@ def test_streams_and_a_captured_graph(api):
     want = api.rms_norm(x, w, 1e-6)
     torch.cuda.synchronize()
     assert torch.equal(got.q, want.q) and torch.equal(got.scale, want.scale)
+
+
+@pytest.mark.parametrize("M,d", [(300, 512), (300, 16384), (300, 16392), (4, 300)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_special_rows_among_many(api, M, d, dtype):
+    """Zeros, tiny, one value, infinities and NaN in each way that rows are taken."""
+    x = _rows(M, d, dtype, 9)
+    x[0] = 0
+    x[1] *= 1e-38
+    x[2] = 0
+    x[2, d - 1] = 3.0
+    bad = [3] if M < 6 else [3, 4, 5]
+    for r, v in zip(bad, (math.nan, -math.inf, math.inf)):
+        x[r, d // 2] = v
+    q, scale = api.quantize_rows(x.to(DEV))
+    ok = torch.ones(M, dtype=torch.bool)
+    ok[bad] = False
+    assert torch.equal(torch.isnan(scale).cpu(), ~ok)
+    assert int(q[bad].abs().max()) == 0 and float(scale[0]) == 0 and int(q[0].abs().max()) == 0
+    ref = x[ok].double().abs().amax(1) / 127
+    assert torch.all((scale.cpu()[ok].double() - ref).abs() <= REL * ref + 2.0 ** -150)
+    t = x[ok].double() / torch.where(ref > 0, ref, 1.0)[:, None]
+    assert float((q.cpu()[ok].double() - t).abs().max()) <= 0.5 + 6e-4
