@@ -125,7 +125,7 @@ struct GemmParams {
   // published through part_flags) before its epilogue.
   int split_start;    // first split unit (== total units when nothing is split)
   int split_k;        // pieces per split tile (1: no split)
-  float* part_buf;    // [n_split][split_k - 1][CTAs per tile][128][BN] fp32
+  float* part_buf;    // [n_split][split_k - 1][CTAs per tile][BN / 4][128][4] fp32
   uint32_t* part_flags;  // [n_split][split_k - 1]
   size_t part_capacity;  // bytes available at part_buf (host side: decides the split)
   const uint8_t* gate;   // [M] per-row adapter gate (0: AR only), or null (all on)
@@ -1341,7 +1341,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         auto slot = [&](int piece) {
           const size_t sl =
               (static_cast<size_t>(x.sidx) * (p.split_k - 1) + (piece - 1)) * nranks + rank;
-          return p.part_buf + sl * (static_cast<size_t>(kBM) * BN) + static_cast<size_t>(rr) * BN;
+          // four columns of every row, then the next four: a warp's 16-byte accesses
+          // are contiguous (row by row they were 1 KB apart, and the split round took
+          // three times a whole one)
+          return p.part_buf + sl * (static_cast<size_t>(kBM) * BN) + static_cast<size_t>(rr) * 4;
         };
         uint32_t* pflags = p.part_flags + static_cast<size_t>(x.sidx) * (p.split_k - 1);
         if (x.piece > 0) {
@@ -1352,7 +1355,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             sm100::tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              __stcg(reinterpret_cast<float4*>(dst + c + e),
+              __stcg(reinterpret_cast<float4*>(dst + (c + e) * kBM),
                      make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
                                  __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])));
           }
@@ -1394,10 +1397,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
           for (int q = 1; q < kMaxSplit; ++q)
             if (q < p.split_k) {
-              const float* src = slot(q) + c;
+              const float* src = slot(q) + c * kBM;
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                f[q - 1][e] = __ldcg(reinterpret_cast<const float4*>(src + 4 * e));
+                f[q - 1][e] = __ldcg(reinterpret_cast<const float4*>(src + 4 * e * kBM));
             }
           uint32_t v[32];
           sm100::tmem_ld_32x32b_x32(acc + lq + c, v);
