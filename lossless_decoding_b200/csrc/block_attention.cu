@@ -73,7 +73,7 @@ constexpr int kMaxT = 4096;    // new tokens per sequence
 constexpr long long kWaitClocks = 2000000000ll;  // bound of every wait: about a second
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kCachedSeqs = 512;  // sequences whose sizes a CTA keeps in shared memory
-constexpr int kLead = 3;       // units that an item's start counts for, in tiles
+constexpr int kLead = 5;       // units that an item's start counts for, in tiles
 constexpr float kLift = 8.f;   // log2 of how far a weight may pass 1 before its row's ref moves
 // Floor of a row's ref: a tile without a finite score leaves it there.
 constexpr float kLowest = -3.0e38f;
@@ -533,6 +533,17 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
       Segment g;
       for (long long u = u0; ok && next_segment(u, g); ++seg) {
         if (warp == kMmaWarp && !need(&q_full[seg & 1], (seg >> 1) & 1)) break;
+        if (g.t0 == 0 && warp > kMmaWarp) {
+          // CTA j begins at unit floor(total j / ctas): inside the item while that is
+          // below its end
+          int n = 0;
+          if (g.end < g.item_end)
+            n = static_cast<int>((g.item_end * s_ctas + s_total - 1) / s_total) -
+                static_cast<int>(blockIdx.x) - 1;
+          const int rts = (a.T * a.G + kRows - 1) / kRows;
+          a.item_ctas[(static_cast<size_t>(g.b) * a.Hkv + g.h) * rts + g.rt] =
+              make_int2(static_cast<int>(blockIdx.x) + 1, n);
+        }
         for (int j = 0; j < g.t1 - g.t0 && ok; ++j, ++it) {
           if (warp == kMmaWarp) scores(it, seg);
           else values(it, j == 0);
@@ -616,16 +627,26 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
       const int t = valid ? r / a.G : 0;
       const uint4* src = reinterpret_cast<const uint4*>(
           a.q + ((static_cast<size_t>(g.b) * a.T + t) * a.Hq + g.h * a.G + (r - t * a.G)) * D);
-      uint32_t top = 0;
-      if (valid) {
-#pragma unroll 4
-        for (int k = 0; k < D / 8; ++k) {
-          const uint4 v = __ldg(src + k);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      // 16-byte pieces at a time: the whole row where the registers hold it (with one
+      // copy they are 80), else a part, read again for the conversion
+      constexpr int kAll = D / 8, kPart = COPIES == 1 ? 8 : kAll;
+      uint4 w[kPart];
+      auto load = [&](int k0) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
-        }
+        for (int k = 0; k < kPart; ++k)
+          w[k] = valid ? __ldg(src + k0 + k) : make_uint4(0u, 0u, 0u, 0u);
+      };
+      uint32_t top = 0;
+#pragma unroll 1
+      for (int k0 = 0; k0 < kAll; k0 += kPart) {
+        load(k0);
+#pragma unroll
+        for (int k = 0; k < kPart; ++k)
+          top = __vmaxu2(__vmaxu2(top, w[k].x & 0x7FFF7FFFu),
+                         __vmaxu2(w[k].y & 0x7FFF7FFFu,
+                                  __vmaxu2(w[k].z & 0x7FFF7FFFu, w[k].w & 0x7FFF7FFFu)));
       }
+      top = max(top & 0xFFFFu, top >> 16);
       const int sh = min(7 + 127 - static_cast<int>(top >> 7), 120);
       const float f = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
       // an infinite or NaN query saturates in e4m3: its scores are NaN instead
@@ -633,28 +654,31 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
           top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
                          : a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
       const uint32_t dst = tmem + lanes + kColQ + (seg & 1) * (D / 2);
-#pragma unroll(COPIES == 1 ? 1 : 4)  // (80 registers hold one block of loads)
-      for (int k = 0; k < D / 32; ++k) {  // 32 elements: 8 columns of each part
-        uint32_t hi[8], lo[8];
+#pragma unroll 1
+      for (int k0 = 0; k0 < kAll; k0 += kPart) {
+        if (kPart < kAll) load(k0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint4 v = valid ? __ldg(src + 4 * k + e) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t h2[4], l2[4];
+        for (int k = 0; k < kPart; k += 4) {  // 32 elements: 8 columns of each part
+          uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float x = bf_lo(w[j]) * f, y = bf_hi(w[j]) * f;
-            h2[j] = e4m3x2(x, y);
-            const float2 back = floats(halves(h2[j]));
-            l2[j] = e4m3x2(x - back.x, y - back.y);
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t x4[4] = {w[k + e].x, w[k + e].y, w[k + e].z, w[k + e].w};
+            uint32_t h2[4], l2[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float x = bf_lo(x4[j]) * f, y = bf_hi(x4[j]) * f;
+              h2[j] = e4m3x2(x, y);
+              const float2 back = floats(halves(h2[j]));
+              l2[j] = e4m3x2(x - back.x, y - back.y);
+            }
+            hi[2 * e] = h2[0] | (h2[1] << 16);
+            hi[2 * e + 1] = h2[2] | (h2[3] << 16);
+            lo[2 * e] = l2[0] | (l2[1] << 16);
+            lo[2 * e + 1] = l2[2] | (l2[3] << 16);
           }
-          hi[2 * e] = h2[0] | (h2[1] << 16);
-          hi[2 * e + 1] = h2[2] | (h2[3] << 16);
-          lo[2 * e] = l2[0] | (l2[1] << 16);
-          lo[2 * e + 1] = l2[2] | (l2[3] << 16);
+          tmem_st<8>(dst + 2 * (k0 + k), hi);
+          tmem_st<8>(dst + D / 4 + 2 * (k0 + k), lo);
         }
-        tmem_st<8>(dst + 8 * k, hi);
-        tmem_st<8>(dst + D / 4 + 8 * k, lo);
       }
       sm100::tmem_st_wait();
       sm100::tc_fence_before();
@@ -768,23 +792,27 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
               if (k + 1 < HC / CH) tmem_ld<CH>(st + c0 + (k + 1) * CH, v[(k + 1) & 1]);
               const float4 x = sc[k];
               const float f = qf * x.x, off = x.y - ref;
-              float sum = 0.f;
+              const uint64_t ff = uno::pack2(f, f), offs = uno::pack2(off, off);
+              uint64_t sums = uno::pack2(0.f, 0.f);
 #pragma unroll
               for (int e = 0; e < CH; e += 2) {
                 const int i = k * CH + e;
-                float t0 = fmaf(__uint_as_float(v[k & 1][e]), f, off);
-                float t1 = fmaf(__uint_as_float(v[k & 1][e + 1]), f, off);
+                const float2 tt = uno::unpack2(uno::fma2(
+                    uno::pack2(__uint_as_float(v[k & 1][e]), __uint_as_float(v[k & 1][e + 1])), ff,
+                    offs));
+                float t0 = tt.x, t1 = tt.y;
                 if constexpr (!decltype(whole)::value) {
                   if (i >= left) t0 = -INFINITY;
                   if (i + 1 >= left) t1 = -INFINITY;
                 }
-                top = fmaxf(top, fmaxf(t0, t1));
+                asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(t0), "f"(t1));
                 t0 = uno::ex2(t0);
                 t1 = uno::ex2(t1);
-                sum += t0 + t1;
+                sums = uno::add2(sums, uno::pack2(t0, t1));
                 pk[i / 2] = pack_f16(t0, t1);
               }
-              add = fmaf(sum, x.z, add);
+              const float2 sum = uno::unpack2(sums);
+              add = fmaf(sum.x + sum.y, x.z, add);
             }
           };
           // A ref moves when any part of a row of the quarter asks for it (the
@@ -872,17 +900,6 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
       }
       // ---- the segment's sums ----
       const int last = it - 1;
-      if (g.t0 == 0 && threadIdx.x == 0) {
-        // CTA j begins at unit floor(total j / ctas): inside the item while that is
-        // below its end
-        int n = 0;
-        if (g.end < g.item_end)
-          n = static_cast<int>((g.item_end * s_ctas + s_total - 1) / s_total) -
-              static_cast<int>(blockIdx.x) - 1;
-        const int rts = (a.T * a.G + kRows - 1) / kRows;
-        a.item_ctas[(static_cast<size_t>(g.b) * a.Hkv + g.h) * rts + g.rt] =
-            make_int2(static_cast<int>(blockIdx.x) + 1, n);
-      }
       need(&o_done[last & 1], (last >> 1) & 1);
       sm100::tc_fence_after();
       if (live) {
