@@ -525,7 +525,7 @@ int uno_block_attention(const void* q, const void* k_new, const void* v_new, con
  * (which correct code never does) sets a bit here, abandons its work and lets
  * the kernel exit instead of hanging the GPU: bit 0 TMA producer, bit 1 MMA
  * issuer, bit 2 epilogue of the dual-path linear, bit 3 TMA producer, bit 4
- * consumer of the block attention. This call synchronises the device, writes the
+ * MMA issuers, bit 5 softmax and decode warps of the block attention. This call synchronises the device, writes the
  * current flags to *flags and clears them when `clear` is non-zero.
  * ------------------------------------------------------------------------ */
 int uno_device_fault_flags(int clear, unsigned int* flags);

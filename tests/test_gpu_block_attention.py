@@ -6,7 +6,10 @@ Against float64. With p the softmax weights, A_old and A_new the weighted sums o
 - n 2^-25 448 max(p v_scale): half's subnormal steps under the largest weight,
 - 2 d (A_old + A_new), d the error of a score in nats: D + 8 float32 roundings
   relative to scale |q| . |k| and four of the score in log2 units, in numerator and
-  denominator alike; the same d covers the float32 sums of n <= 2^17 terms by
+  denominator alike; over cached tokens also the queries' two e4m3 parts, which drop
+  what is below half a subnormal step, 2^-10, with the row's largest element at
+  128 or more, so at most 2^-17 max|q| of each element: 2^-17 scale max|q| sum|k|;
+  the same d covers the float32 sums of n <= 2^17 terms by
   16 (tiles and shuffles chain fewer than 2^13 additions of positive terms,
   each rounding a part of the sum) steps of 2^-24 times 2^9,
 - half a bfloat16 step of the output.
@@ -112,6 +115,9 @@ def _check(out, q, k, v, c, lens, parent=None, num_new=None, scale=None):
                 mag = (Q.abs() @ K.abs().t()).amax(1, keepdim=True) * abs(scale)
                 d = (D + 8) * 2.0 ** -24 * mag + 4 * 2.0 ** -24 * z.abs().amax(1, keepdim=True) \
                     + 2.0 ** -11 * 2.0 ** -1
+                if n:
+                    d = d + 2.0 ** -17 * abs(scale) * Q.abs().amax(1, keepdim=True) * \
+                        K[:n].abs().sum(1).amax()
                 top = torch.cat([p[:, :n] * vs, p[:, n:]], 1).amax(1, keepdim=True)
                 tol = 2.0 ** -11 * a_old + 2.0 ** -8 * a_new + (n + m) * 2.0 ** -25 * 448 * top \
                     + 2 * d * (a_old + a_new) + 2.0 ** -8 * ref.abs() + 1e-38
@@ -174,6 +180,32 @@ def test_long_caches_split_over_many_ctas(api, lens, H, T):
 
 def test_many_short_sequences(api):
     _run(api, [(37 * i) % 200 for i in range(150)], 2, 4, 1, 64, 16, seed=8)
+
+
+def test_more_sequences_than_a_cta_keeps_in_shared_memory(api):
+    """Their sizes are then read from memory; most sequences here are empty or unused."""
+    B = 1100
+    lens = [0] * B
+    nodes = [0] * B
+    for b in (0, 31, 32, 511, 512, 513, 700, 1099):
+        lens[b], nodes[b] = 20 + b % 37, 1 + b % 2
+    _run(api, lens, 2, 4, 1, 64, 32, seed=40, nodes=nodes)
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_a_non_finite_query_row_stays_alone(api, bad):
+    lens = [200, 0]
+    c = _cache(api, lens, 4, 2, 64, 128, seed=41)
+    q, k, v = _new(2, 5, 8, 2, 128, 42)
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    clean = api.block_attention(q, k, v, c, ln)
+    q[0, 2, 3, 17] = q[1, 4, 6, 0] = bad
+    out = api.block_attention(q, k, v, c, ln)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[0, 2, 3]).all() and torch.isnan(out[1, 4, 6]).all()
+    keep = torch.ones(2, 5, 8, dtype=torch.bool, device=DEV)
+    keep[0, 2, 3] = keep[1, 4, 6] = False
+    assert torch.equal(out[keep], clean[keep])
 
 
 @pytest.mark.parametrize("spread", [3, 20])
