@@ -60,9 +60,9 @@ constexpr int kStages = 4;     // tiles of codes in shared memory
 constexpr int kProducers = 2;  // TMA warps, alternating tiles
 // Warps of cached_kernel: 4 parts() for the softmax (TMEM lane quarter = warp % 4, part
 // of a row's tokens = warp / 4), decoders() for the value decode (the first four of them
-// for the queries too), the producers, and two MMA issuers (scores; weighted values): a thread that has issued products
-// waits at its next barrier until they are done, so one issuer would leave the
-// tensor pipe idle between the two.
+// for the queries too), the producers, and two MMA issuers (scores; weighted values): a
+// thread that has issued products waits at its next barrier until they are done, so one
+// issuer would leave the tensor pipe idle between the two.
 __host__ __device__ constexpr int parts(int copies) { return copies == 1 ? 4 : 1; }
 __host__ __device__ constexpr int decoders(int copies) { return copies == 1 ? 4 : 8; }
 constexpr int threads(int copies) {
@@ -73,7 +73,9 @@ constexpr int kMaxT = 4096;    // new tokens per sequence
 constexpr long long kWaitClocks = 2000000000ll;  // bound of every wait: about a second
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kCachedSeqs = 512;  // sequences whose sizes a CTA keeps in shared memory
-constexpr int kLead = 5;       // units that an item's start counts for, in tiles
+// Units that an item's start counts for, in tiles (32 single tokens of lengths 1 to
+// 8191: 94 us with 3, 86 us with 4 or 5).
+constexpr int kLead = 5;
 constexpr float kLift = 8.f;   // log2 of how far a weight may pass 1 before its row's ref moves
 // Floor of a row's ref: a tile without a finite score leaves it there.
 constexpr float kLowest = -3.0e38f;
@@ -338,10 +340,15 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
   constexpr int DECODERS = decoders(COPIES);
   constexpr int kFirstDecode = 4 * PARTS, kFirstProducer = kFirstDecode + DECODERS;
   constexpr int kMmaWarp = kFirstProducer + kProducers;  // scores (and TMEM); + 1: values
-  // TMEM columns: two score tiles (their weights over them), o, the queries' parts
-  // of two segments
-  constexpr uint32_t kColO = 2 * kTile, kColQ = kColO + D;
-  static_assert(kColQ + D <= 512, "TMEM columns");
+  // TMEM columns: two score tiles, o, then either the queries' parts of two segments,
+  // with a tile's weights over its scores, or those of one segment and weights of
+  // their own. The latter (row copies) lets a tile's scores follow as soon as the one two
+  // before has been read, without its weighted values, for a softmax that is shorter
+  // than the products; the next segment's queries then come late, but the epilogue of
+  // the segment before takes longer still.
+  constexpr bool kOwnWeights = COPIES > 1;
+  constexpr uint32_t kColO = 2 * kTile, kColQ = kColO + D, kColP = kColQ + D / 2;
+  static_assert(kColQ + D <= 512 && kColP + kTile / 2 <= 512, "TMEM columns");
   constexpr uint32_t kIdescS = (1u << 4) | ((kTile >> 3) << 17) | ((kRows >> 4) << 24);
   constexpr uint32_t kIdescO =
       (1u << 4) | (1u << 16) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((kRows >> 4) << 24);
@@ -503,12 +510,14 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
       auto scores = [&](int it, int seg) {
         const int s = it % kStages;
         if (!need(&full[s], (it / kStages) & 1)) return;
-        // the tile's columns held the weights of tile it - 2
-        if (it >= 2 && !need(&o_done[it & 1], ((it >> 1) - 1) & 1)) return;
+        // the tile's columns held the scores of tile it - 2 (and its weights)
+        if (it >= 2 &&
+            !need(kOwnWeights ? &pv_full[it & 1] : &o_done[it & 1], ((it >> 1) - 1) & 1))
+          return;
         sm100::tc_fence_after();
         const uint64_t kd = key_desc<D>(sm100::smem_addr(smem + s * P::kStage));
         const uint32_t d = tmem + (it & 1) * kTile;
-        const uint32_t q = tmem + kColQ + (seg & 1) * (D / 2);
+        const uint32_t q = tmem + kColQ + (kOwnWeights ? 0 : (seg & 1) * (D / 2));
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -525,8 +534,8 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
             value_desc(sm100::smem_addr(smem + P::kDecoded + k2 * P::kHalfTile));
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)  // 16 tokens: 8 columns of weights, 2048 bytes
-          mma_ts<false>(tmem + kColO, tmem + k2 * kTile + 8 * k, vd + k * 128, kIdescO,
-                        !first || k > 0);
+          mma_ts<false>(tmem + kColO, tmem + (kOwnWeights ? kColP : k2 * kTile) + 8 * k,
+                        vd + k * 128, kIdescO, !first || k > 0);
         sm100::mma_commit(&o_done[k2]);
       };
       int it = 0, seg = 0;
@@ -618,7 +627,8 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
     // ---- queries of a segment to e4m3 parts, codes of a tile's values to halves ----
     const int tid = threadIdx.x - 32 * kFirstDecode;
     const uint32_t lanes = static_cast<uint32_t>(tid & 96) << 16;
-    // (the first four warps) The queries of segment `seg`, in the columns that those of segment seg - 2 have left.
+    // (the first four warps) The queries of segment `seg`, in columns that an earlier
+    // segment's have left.
     auto stage_queries = [&](const Segment& g, int seg) {
       if (tid >= 128) return;
       // q 2^sh = hi + lo, its largest magnitude in [128, 256)
@@ -653,7 +663,7 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
       s_factor[(seg & 1) * kRows + tid] =
           top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
                          : a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-      const uint32_t dst = tmem + lanes + kColQ + (seg & 1) * (D / 2);
+      const uint32_t dst = tmem + lanes + kColQ + (kOwnWeights ? 0 : (seg & 1) * (D / 2));
 #pragma unroll 1
       for (int k0 = 0; k0 < kAll; k0 += kPart) {
         if (kPart < kAll) load(k0);
@@ -732,10 +742,12 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
           sm100::mbar_arrive(&pv_full[k2]);
           sm100::mbar_arrive(&empty[s]);
         }
-        if (more && tid < 128 && ti == min(g.t0 + 1, g.t1 - 1)) {
-          // the next segment's queries go where the one before's were; its products are
-          // done once its last tile's weighted values are
-          if (before >= 0 && !wait(&o_done[before & 1], (before >> 1) & 1)) {
+        if (more && tid < 128 && ti == (kOwnWeights ? g.t1 - 1 : min(g.t0 + 1, g.t1 - 1))) {
+          // The next segment's queries, once the products of those that they replace are
+          // done: this segment's with its last scores, the one before's with its last
+          // weighted values.
+          if (kOwnWeights ? !wait(&s_full[k2], (it >> 1) & 1)
+                          : before >= 0 && !wait(&o_done[before & 1], (before >> 1) & 1)) {
             give_up(kFaultSoftmax);
             ok = false;
             break;
@@ -755,13 +767,26 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
     constexpr int CH = 16;  // of which it loads so many at once
     int it = 0, seg = 0;
     bool ok = true;  // false: go on without waiting, the results are abandoned
+    // (each lane for itself, and mostly for a phase that is over: a vote as in wait()
+    // costs as much as the test)
     auto need = [&](uint64_t* bar, uint32_t parity) {
-      if (ok && !wait(bar, parity)) {
-        give_up(kFaultSoftmax);
+      if (!phase_done(bar, parity) && ok && !wait_one(bar, parity)) {
+        atomicOr(&g_attn_fault, kFaultSoftmax);
+        s_abort = 1;
         ok = false;
       }
+      __syncwarp();
     };
     Segment g;
+    if constexpr (kOwnWeights) {
+      // the other copies' tokens have weight 0, in every tile
+#pragma unroll
+      for (int k = 0; k < kTile / 32; ++k) {
+        const uint32_t z[16] = {};
+        tmem_st<16>(tmem + lanes + kColP + 16 * k, z);
+      }
+      sm100::tmem_st_wait();
+    }
     for (long long u = u0; next_segment(u, g); ++seg) {
       const int r = g.rt * kRows + my_row;  // row of the sequence and KV head
       const bool valid = r < g.s.nn * a.G;
@@ -879,15 +904,13 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
             if (!move) break;
           }
           l += add;
-          tmem_st<HC / 2>(st + c0 / 2, pk);
-          if constexpr (COPIES > 1) {
-            // the other copies' tokens get weight 0
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (k / (4 / COPIES) != copy) {
-                const uint32_t z[16] = {};
-                tmem_st<16>(st + 16 * k, z);
-              }
+          if constexpr (kOwnWeights) {
+            // tile it - 1's weights have been used
+            if (it > 0) need(&o_done[k2 ^ 1], ((it - 1) >> 1) & 1);
+            sm100::tc_fence_after();
+            tmem_st<HC / 2>(tmem + lanes + kColP + c0 / 2, pk);
+          } else {
+            tmem_st<HC / 2>(st + c0 / 2, pk);
           }
           sm100::tmem_st_wait();
         }
