@@ -30,7 +30,8 @@
 // the decode would go, but splitting a weight costs the softmax warps more than
 // the decode costs (7 clocks an element against 1).
 //
-// Softmax. A row is a thread. Value scales go into the exponent: t = score
+// Softmax. A lane holds a row, and the warps of a lane quarter share the tile's
+// tokens, each with a running maximum and sum of its own. Value scales go into the exponent: t = score
 // log2(e) + log2(v_scale), p = 2^(t - ref), and the normaliser sums p / v_scale in
 // float32. ref moves only when a tile's largest t exceeds it by 8 (then o and l
 // are rescaled and the tile's weights taken again), so the common tile is one
