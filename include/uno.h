@@ -393,8 +393,9 @@ int uno_tree_verify(const void* p_logits, const int32_t* node_token, const int32
  *   scale = max|y| / 127,  q = y / scale rounded to nearest even, |q| <= 127
  * uno_quantize_rows is the last line alone, for inputs that no norm writes
  * (attention outputs, MLP activations). A row of zeros has scale 0 and q 0. A
- * row with an infinity or NaN, or whose sum of squares passes float32, has
- * scale NaN and q 0.
+ * row with an infinity or NaN (in the input, in h w, or because its sum of
+ * squares passes float32) has scale NaN and q 0, and so has, with eps = 0, a
+ * row whose squares are all 0 in float32.
  *
  * x, residual  [M, d] dtype
  * w            [d] dtype
@@ -504,6 +505,7 @@ int uno_kv_append(const void* k_new, const void* v_new, const int32_t* start,
  * lens[b] may hold infinities and NaN.
  * Limits: B <= 65535, T <= 4096, Hkv <= 1024, Hq <= 16384 a multiple of Hkv, D 64 or
  * 128, page 16, 32, 64 or 128, width * page <= 2^30, num_pages * Hkv * page < 2^31.
+ *              out shares no memory with an input
  * workspace    at least uno_block_attention_workspace_bytes(...) bytes, 16-byte
  *              aligned, contents irrelevant on entry. Two calls that share one
  *              must be ordered on one stream.

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(1024) row_quant_kernel(const RowArgs a, int wa
   }
   if (!a.q) return;
   const float amax = __uint_as_float(top);
-  const bool bad = top >= 0x7F800000u || !(sum < INFINITY);
+  const bool bad = top >= 0x7F800000u || !(sum < INFINITY) || !(rstd < INFINITY);
   const float inv = bad ? 0.f : 127.f / amax;
   constexpr float kRound = 12582912.f;  // 1.5 * 2^23: an integer added to it stays in the low bits
   int8_t* dst = a.q + at + tid * V;
@@ -308,8 +308,8 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) quant_bf16_kernel(con
                           lane < static_cast<int>(blockDim.x) / 32 ? s_max[lane] : 0u);
   const float amax = uno::bf16_bits_to_float(top);
   const bool bad = top >= 0x7F80u;
-  // (bfloat16's smallest magnitudes divide: 127 / amax passes float32)
-  const bool tiny = top < 0x0200u;
+  // (below 2^-121 127 / amax passes float32: such rows are lifted by 2^64 first)
+  const bool tiny = top < 0x0300u;
   const float inv = bad || top == 0 ? 0.f : tiny ? 127.f / (amax * 0x1p64f) : 127.f / amax;
   const float lift = tiny ? 0x1p64f : 1.f;
   constexpr float kRound = 12582912.f;

@@ -167,3 +167,31 @@ def test_special_rows_among_many(api, M, d, dtype):
     assert torch.all((scale.cpu()[ok].double() - ref).abs() <= REL * ref + 2.0 ** -150)
     t = x[ok].double() / torch.where(ref > 0, ref, 1.0)[:, None]
     assert float((q.cpu()[ok].double() - t).abs().max()) <= 0.5 + 6e-4
+
+
+@pytest.mark.parametrize("M,d", [(4, 512), (300, 512), (300, 4096), (300, 41)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_every_binade_where_127_over_the_maximum_nears_float32s_end(api, M, d, dtype):
+    # maxima of 2^-126 to 2^-115: 127 / max passes float32 below 127 / FLT_MAX, just under 2^-121
+    for e in range(-126, -114):
+        x = _rows(M, d, dtype, 100 - e).clamp(-1.5, 1.5) * 2.0 ** e
+        x[:, 0] = 1.75 * 2.0 ** e
+        x[1, 1] = 0
+        q, scale = api.quantize_rows(x.to(DEV))
+        ref = x.double().abs().amax(1) / 127
+        # the scale is a subnormal number: half a step of 2^-149
+        assert torch.all((scale.cpu().double() - ref).abs() <= REL * ref + 2.0 ** -150), e
+        assert float((q.cpu().double() - x.double() / ref[:, None]).abs().max()) <= 0.5 + 6e-4, e
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_without_eps_of_rows_whose_squares_vanish(api, dtype):
+    x = _rows(4, 264, dtype, 30)
+    x[1] = 0
+    x[2] *= 1e-30
+    w = torch.ones(264, dtype=DT[dtype])
+    r = api.rms_norm(x.to(DEV), w.to(DEV), 0.0)
+    assert torch.isnan(r.scale).tolist() == [False, True, True, False]
+    assert int(r.q[1:3].abs().max()) == 0
+    _, y, scale = rms_norm(x[3:], w, 0.0)
+    _check_q(r.q[3:], r.scale[3:], y, scale)
