@@ -746,9 +746,11 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
         if (more && tid < 128 && ti == (kOwnWeights ? g.t1 - 1 : min(g.t0 + 1, g.t1 - 1))) {
           // The next segment's queries, once the products of those that they replace are
           // done: this segment's with its last scores, the one before's with its last
-          // weighted values.
+          // weighted values. (From a segment's second tile on that has been waited for
+          // above; asked again now, this tile's own could have ended a phase later.)
           if (kOwnWeights ? !wait(&s_full[k2], (it >> 1) & 1)
-                          : before >= 0 && !wait(&o_done[before & 1], (before >> 1) & 1)) {
+                          : ti == g.t0 && before >= 0 &&
+                                !wait(&o_done[before & 1], (before >> 1) & 1)) {
             give_up(kFaultSoftmax);
             ok = false;
             break;
