@@ -46,6 +46,7 @@
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "sm100.cuh"
@@ -72,6 +73,7 @@ constexpr int threads(int copies) {
 constexpr int kMaxCtas = 148;  // one CTA per SM
 constexpr int kMaxT = 4096;    // new tokens per sequence
 constexpr long long kWaitClocks = 2000000000ll;  // bound of every wait: about a second
+constexpr int kFewN = 16;  // columns of the products of few rows
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kCachedSeqs = 512;  // sequences whose sizes a CTA keeps in shared memory
 // Units that an item's start counts for, in tiles (32 single tokens of lengths 1 to
@@ -183,6 +185,23 @@ __device__ __forceinline__ float2 floats(uint32_t halves2) {
   return f;
 }
 
+// The queries' two e4m3 parts, q 2^sh = hi + lo with the row's largest magnitude (top, its
+// bfloat16 bits) in [128, 256), and what takes their scores back to log2 of a weight.
+__device__ __forceinline__ int query_shift(uint32_t top) {
+  return min(7 + 127 - static_cast<int>(top >> 7), 120);
+}
+__device__ __forceinline__ float query_factor(float scale, uint32_t top, int sh) {
+  // an infinite or NaN query saturates in e4m3: its scores are NaN instead
+  return top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
+                        : scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+}
+__device__ __forceinline__ void split_e4m3(uint32_t pair, float f, uint32_t& hi, uint32_t& lo) {
+  const float x = bf_lo(pair) * f, y = bf_hi(pair) * f;
+  hi = e4m3x2(x, y);
+  const float2 back = floats(halves(hi));
+  lo = e4m3x2(x - back.x, y - back.y);
+}
+
 __device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -244,6 +263,16 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
   }
 }
 
+// D[tmem] (+)= A[smem desc] B[smem desc] on e4m3 codes, one thread.
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+
 // D[tmem] (+)= A[tmem] B[smem desc], one thread. kF8: kind::f8f6f4, else kind::f16.
 template <bool kF8>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc,
@@ -297,9 +326,10 @@ __device__ __forceinline__ uint64_t key_desc(uint32_t saddr) {
   d |= static_cast<uint64_t>(D == 128 ? 2u : 4u) << 61;
   return d;
 }
+template <bool kTwice = false>  // kTwice: the first 64 columns again for the second
 __device__ __forceinline__ uint64_t value_desc(uint32_t saddr) {
   uint64_t d = (saddr >> 4) & 0x3FFFu;
-  d |= static_cast<uint64_t>((kTile * 128) >> 4) << 16;
+  d |= static_cast<uint64_t>(kTwice ? 0 : (kTile * 128) >> 4) << 16;
   d |= static_cast<uint64_t>(1024u >> 4) << 32;
   d |= static_cast<uint64_t>(1u) << 46;
   d |= static_cast<uint64_t>(2u) << 61;
@@ -309,12 +339,17 @@ __device__ __forceinline__ uint64_t value_desc(uint32_t saddr) {
 // Shared memory: [stage]{keys, values}, two tiles of decoded values, scales
 // [stage][16-token group], the rows' score factors [segment parity][lane], what the
 // parts of a row tell each other, barriers.
-template <int D>
+template <int D, int FEW = 0>
 struct Plan {
   static constexpr int kStage = 2 * kTile * D;
   static constexpr int kHalfTile = kTile * D * 2;
   static constexpr int kDecoded = kStages * kStage;
-  static constexpr int kScales = kDecoded + 2 * kHalfTile;
+  // (few rows) [segment parity][part][kFewN rows][D] codes; [tile parity] weights
+  static constexpr int kQueries = kDecoded + 2 * kHalfTile;
+  static constexpr int kQueryPart = kFewN * D;
+  static constexpr int kWeights = kQueries + (FEW ? 4 * kQueryPart : 0);
+  static constexpr int kWeightTile = kFewN * kTile * 2;
+  static constexpr int kScales = kWeights + (FEW ? 2 * kWeightTile : 0);
   static constexpr int kFactors = kScales + kStages * (kTile / 16) * 16;
   static constexpr int kTops = kFactors + 2 * kRows * 4;  // [part][lane]
   static constexpr int kFlags = kTops + 4 * kRows * 4;    // [tile parity][quarter][part]
@@ -330,11 +365,13 @@ __device__ __forceinline__ int row_of_lane(int lane) {
   return lane & (kRows / COPIES - 1);
 }
 
-template <int D, int COPIES>
+// FEW > 0: at most FEW rows, tokens on the lanes (COPIES is 2 then, for the warps' roles,
+// and the sums are one copy).
+template <int D, int COPIES, int FEW>
 __global__ void __launch_bounds__(threads(COPIES), 1)
     cached_kernel(const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const AttnArgs a) {
-  using P = Plan<D>;
+  using P = Plan<D, FEW>;
   constexpr int CW = kTile / COPIES;  // a row copy's tokens per tile
   constexpr int PARTS = parts(COPIES);
   constexpr int HC = CW / PARTS;      // a softmax thread's
@@ -348,11 +385,19 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
   // than the products; the next segment's queries then come late, but the epilogue of
   // the segment before takes longer still.
   constexpr bool kOwnWeights = COPIES > 1;
+  constexpr bool kLateQueries = kOwnWeights && !FEW;
   constexpr uint32_t kColO = 2 * kTile, kColQ = kColO + D, kColP = kColQ + D / 2;
   static_assert(kColQ + D <= 512 && kColP + kTile / 2 <= 512, "TMEM columns");
   constexpr uint32_t kIdescS = (1u << 4) | ((kTile >> 3) << 17) | ((kRows >> 4) << 24);
   constexpr uint32_t kIdescO =
       (1u << 4) | (1u << 16) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((kRows >> 4) << 24);
+  // few rows: keys (tokens x D) times queries, and values (D x tokens, the values'
+  // descriptor on the A side) times weights
+  constexpr uint32_t kColFewO = 2 * kFewN;
+  constexpr uint32_t kIdescFewS = (1u << 4) | ((kFewN >> 3) << 17) | ((kRows >> 4) << 24);
+  constexpr uint32_t kIdescFewO =
+      (1u << 4) | (1u << 15) | ((kFewN >> 3) << 17) | ((kRows >> 4) << 24);
+  constexpr uint32_t kTmemCols = FEW ? 64 : 512;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -389,7 +434,7 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
     s_abort = 0;
     sm100::fence_mbar_init();
   }
-  if (warp == kMmaWarp) sm100::tmem_alloc(tmem_holder, 512);
+  if (warp == kMmaWarp) sm100::tmem_alloc(tmem_holder, kTmemCols);
   if (warp == kFirstProducer && lane < 2) sm100::tma_prefetch_desc(lane ? &map_v : &map_k);
   uno::grid_dependency_wait();
   // finish_kernel may start: what it reads before its own wait is older than this launch
@@ -517,13 +562,24 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
           return;
         sm100::tc_fence_after();
         const uint64_t kd = key_desc<D>(sm100::smem_addr(smem + s * P::kStage));
-        const uint32_t d = tmem + (it & 1) * kTile;
-        const uint32_t q = tmem + kColQ + (kOwnWeights ? 0 : (seg & 1) * (D / 2));
+        if constexpr (FEW > 0) {
+          const uint64_t qd = key_desc<D>(
+              sm100::smem_addr(smem + P::kQueries + (seg & 1) * 2 * P::kQueryPart));
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+          for (int part = 0; part < 2; ++part)
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k)  // 32 codes: 32 bytes, 8 columns of queries
-            mma_ts<true>(d, q + part * (D / 4) + 8 * k, kd + 2 * k, kIdescS, part + k > 0);
+            for (int k = 0; k < D / 32; ++k)
+              mma_f8(tmem + (it & 1) * kFewN, kd + 2 * k, qd + part * (P::kQueryPart >> 4) + 2 * k,
+                     kIdescFewS, part + k > 0);
+        } else {
+          const uint32_t d = tmem + (it & 1) * kTile;
+          const uint32_t q = tmem + kColQ + (kOwnWeights ? 0 : (seg & 1) * (D / 2));
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)  // 32 codes: 32 bytes, 8 columns of queries
+              mma_ts<true>(d, q + part * (D / 4) + 8 * k, kd + 2 * k, kIdescS, part + k > 0);
+        }
         sm100::mma_commit(&s_full[it & 1]);
         sm100::mma_commit(&empty[s]);
       };
@@ -532,11 +588,22 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
         if (!need(&pv_full[k2], (it >> 1) & 1)) return;
         sm100::tc_fence_after();
         const uint64_t vd =
-            value_desc(sm100::smem_addr(smem + P::kDecoded + k2 * P::kHalfTile));
+            value_desc<FEW && D == 64>(
+                sm100::smem_addr(smem + P::kDecoded + k2 * P::kHalfTile));
+        if constexpr (FEW > 0) {
+          const uint64_t wd =
+              key_desc<128>(sm100::smem_addr(smem + P::kWeights + k2 * P::kWeightTile));
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)  // 16 tokens: 8 columns of weights, 2048 bytes
-          mma_ts<false>(tmem + kColO, tmem + (kOwnWeights ? kColP : k2 * kTile) + 8 * k,
-                        vd + k * 128, kIdescO, !first || k > 0);
+          for (int k = 0; k < kTile / 16; ++k)  // 16 tokens: 32 bytes of weights
+            sm100::mma<false>(tmem + kColFewO, vd + k * 128,
+                              wd + (k >> 2) * (P::kWeightTile / 2 >> 4) + 2 * (k & 3), kIdescFewO,
+                              !first || k > 0);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)  // 16 tokens: 8 columns of weights, 2048 bytes
+            mma_ts<false>(tmem + kColO, tmem + (kOwnWeights ? kColP : k2 * kTile) + 8 * k,
+                          vd + k * 128, kIdescO, !first || k > 0);
+        }
         sm100::mma_commit(&o_done[k2]);
       };
       int it = 0, seg = 0;
@@ -632,6 +699,49 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
     // segment's have left.
     auto stage_queries = [&](const Segment& g, int seg) {
       if (tid >= 128) return;
+      if constexpr (FEW > 0) {
+        // eight threads to a row, D / 8 elements each, to the codes' layout of keys
+        constexpr int kW = D / 64;  // 16-byte pieces
+        const int r = tid >> 3, part = tid & 7;
+        const bool valid = r < g.s.nn * a.G;
+        const int t = valid ? r / a.G : 0;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + ((static_cast<size_t>(g.b) * a.T + t) * a.Hq + g.h * a.G + (r - t * a.G)) * D +
+            part * (D / 8));
+        uint4 w[kW];
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < kW; ++k) {
+          w[k] = valid ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+          top = __vmaxu2(__vmaxu2(top, w[k].x & 0x7FFF7FFFu),
+                         __vmaxu2(w[k].y & 0x7FFF7FFFu,
+                                  __vmaxu2(w[k].z & 0x7FFF7FFFu, w[k].w & 0x7FFF7FFFu)));
+        }
+        top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        const int sh = query_shift(top);
+        const float f = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
+        if (part == 0) s_factor[(seg & 1) * kRows + r] = query_factor(a.scale, top, sh);
+        uint8_t* dst = smem + P::kQueries + (seg & 1) * 2 * P::kQueryPart + r * D;
+#pragma unroll
+        for (int k = 0; k < kW; ++k) {  // 8 codes of each part
+          const uint32_t x4[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+          uint32_t h2[4], l2[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) split_e4m3(x4[j], f, h2[j], l2[j]);
+          const int at = part * (D / 8) + 8 * k;  // byte of the row, 16-byte chunks swizzled
+          const int sw = D == 128 ? (r & 7) : ((r >> 1) & 3);
+          uint8_t* p = dst + ((((at >> 4) ^ sw) << 4) | (at & 15));
+          *reinterpret_cast<uint2*>(p) = make_uint2(h2[0] | (h2[1] << 16), h2[2] | (h2[3] << 16));
+          *reinterpret_cast<uint2*>(p + P::kQueryPart) =
+              make_uint2(l2[0] | (l2[1] << 16), l2[2] | (l2[3] << 16));
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(&q_full[seg & 1]);
+        return;
+      }
       // q 2^sh = hi + lo, its largest magnitude in [128, 256)
       const int r = g.rt * kRows + row_of_lane<COPIES>(tid);
       const bool valid = r < g.s.nn * a.G;
@@ -658,12 +768,9 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
                                   __vmaxu2(w[k].z & 0x7FFF7FFFu, w[k].w & 0x7FFF7FFFu)));
       }
       top = max(top & 0xFFFFu, top >> 16);
-      const int sh = min(7 + 127 - static_cast<int>(top >> 7), 120);
+      const int sh = query_shift(top);
       const float f = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
-      // an infinite or NaN query saturates in e4m3: its scores are NaN instead
-      s_factor[(seg & 1) * kRows + tid] =
-          top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
-                         : a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+      s_factor[(seg & 1) * kRows + tid] = query_factor(a.scale, top, sh);
       const uint32_t dst = tmem + lanes + kColQ + (kOwnWeights ? 0 : (seg & 1) * (D / 2));
 #pragma unroll 1
       for (int k0 = 0; k0 < kAll; k0 += kPart) {
@@ -676,12 +783,7 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
             const uint32_t x4[4] = {w[k + e].x, w[k + e].y, w[k + e].z, w[k + e].w};
             uint32_t h2[4], l2[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float x = bf_lo(x4[j]) * f, y = bf_hi(x4[j]) * f;
-              h2[j] = e4m3x2(x, y);
-              const float2 back = floats(halves(h2[j]));
-              l2[j] = e4m3x2(x - back.x, y - back.y);
-            }
+            for (int j = 0; j < 4; ++j) split_e4m3(x4[j], f, h2[j], l2[j]);
             hi[2 * e] = h2[0] | (h2[1] << 16);
             hi[2 * e + 1] = h2[2] | (h2[3] << 16);
             lo[2 * e] = l2[0] | (l2[1] << 16);
@@ -743,12 +845,12 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
           sm100::mbar_arrive(&pv_full[k2]);
           sm100::mbar_arrive(&empty[s]);
         }
-        if (more && tid < 128 && ti == (kOwnWeights ? g.t1 - 1 : min(g.t0 + 1, g.t1 - 1))) {
+        if (more && tid < 128 && ti == (kLateQueries ? g.t1 - 1 : min(g.t0 + 1, g.t1 - 1))) {
           // The next segment's queries, once the products of those that they replace are
           // done: this segment's with its last scores, the one before's with its last
           // weighted values. (From a segment's second tile on that has been waited for
           // above; asked again now, this tile's own could have ended a phase later.)
-          if (kOwnWeights ? !wait(&s_full[k2], (it >> 1) & 1)
+          if (kLateQueries ? !wait(&s_full[k2], (it >> 1) & 1)
                           : ti == g.t0 && before >= 0 &&
                                 !wait(&o_done[before & 1], (before >> 1) & 1)) {
             give_up(kFaultSoftmax);
@@ -758,6 +860,139 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
           stage_queries(next, seg + 1);
         }
       }
+    }
+  } else if constexpr (FEW > 0) {
+    // ---- softmax of few rows: a token per thread, its weights for every row ----
+    const int tok = threadIdx.x;  // token of a tile, and TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    int it = 0, seg = 0;
+    bool ok = true;  // false: go on without waiting, the results are abandoned
+    auto need = [&](uint64_t* bar, uint32_t parity) {
+      if (!phase_done(bar, parity) && ok && !wait_one(bar, parity)) {
+        atomicOr(&g_attn_fault, kFaultSoftmax);
+        s_abort = 1;
+        ok = false;
+      }
+      __syncwarp();
+    };
+    auto all_meet = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    // weights of a tile: [half of the tokens][row][64 tokens], 16-byte chunks swizzled
+    uint8_t* const wrow = smem + P::kWeights + (tok >> 6) * (P::kWeightTile / 2) + (tok & 7) * 2;
+    const int chunk = (tok & 63) >> 3;
+    Segment g;
+    for (long long u = u0; next_segment(u, g); ++seg) {
+      need(&q_full[seg & 1], (seg >> 1) & 1);
+      float qf[FEW], ref[FEW], l[FEW];
+#pragma unroll
+      for (int n = 0; n < FEW; ++n) {
+        qf[n] = s_factor[(seg & 1) * kRows + n];
+        ref[n] = kLowest;
+        l[n] = 0.f;
+      }
+      for (int ti = g.t0; ti < g.t1; ++ti, ++it) {
+        const int s = it % kStages, k2 = it & 1;
+        need(&full[s], (it / kStages) & 1);  // the scales
+        const float4 x = s_scale[s * (kTile / 16) + tok / 16];
+        const bool in = ti * kTile + tok < g.s.len;
+        need(&s_full[k2], (it >> 1) & 1);
+        sm100::tc_fence_after();
+        uint32_t v[16];
+        tmem_ld<16>(tmem + lanes + k2 * kFewN, v);
+        sm100::tmem_ld_wait();
+        float t[FEW];
+#pragma unroll
+        for (int n = 0; n < FEW; ++n)
+          t[n] = in ? fmaf(__uint_as_float(v[n]), qf[n] * x.x, x.y) : -INFINITY;
+        bool move = ti == g.t0;  // the first tile sets the refs
+        if (!move) {
+          // they move when any token asks for it (the flags alternate with the tiles, so
+          // a meeting later they may be rewritten)
+          float top = -INFINITY;
+#pragma unroll
+          for (int n = 0; n < FEW; ++n) top = fmaxf(top, t[n] - ref[n]);
+          const bool ask = __any_sync(0xFFFFFFFFu, top > kLift);
+          if (lane == 0) s_flag[k2 * 4 + warp] = ask;
+          all_meet();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) move |= s_flag[k2 * 4 + k] != 0;
+        }
+        if (move) {
+#pragma unroll
+          for (int n = 0; n < FEW; ++n) {
+            float mx = fmaxf(t[n], kLowest);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+            if (lane == 0) s_top[warp * kRows + n] = mx;
+          }
+          all_meet();  // (read before the next write: a tile's flags or a segment's end lie between)
+          float al[FEW];
+#pragma unroll
+          for (int n = 0; n < FEW; ++n) {
+            float mx = s_top[n];
+#pragma unroll
+            for (int k = 1; k < 4; ++k) mx = fmaxf(mx, s_top[k * kRows + n]);
+            const float to = ti == g.t0 || mx > ref[n] + kLift ? mx : ref[n];
+            al[n] = uno::ex2(ref[n] - to);
+            ref[n] = to;
+            l[n] *= al[n];
+          }
+          if (ti > g.t0) {
+            // o holds the tiles before this one once the last of them has been added
+            need(&o_done[k2 ^ 1], ((it - 1) >> 1) & 1);
+            sm100::tc_fence_after();
+            tmem_ld<16>(tmem + lanes + kColFewO, v);
+            sm100::tmem_ld_wait();
+#pragma unroll
+            for (int n = 0; n < FEW; ++n) v[n] = __float_as_uint(__uint_as_float(v[n]) * al[n]);
+            tmem_st<16>(tmem + lanes + kColFewO, v);
+            sm100::tmem_st_wait();
+          }
+        }
+        if (it >= 2) need(&o_done[k2], ((it >> 1) - 1) & 1);  // the weights of tile it - 2
+#pragma unroll
+        for (int n = 0; n < FEW; ++n) {
+          const float w = uno::ex2(t[n] - ref[n]);
+          l[n] = fmaf(w, x.z, l[n]);
+          *reinterpret_cast<__half*>(wrow + k2 * P::kWeightTile + n * 128 +
+                                     ((chunk ^ (n & 7)) << 4)) = __float2half_rn(w);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        sm100::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          sm100::mbar_arrive(&pv_full[k2]);
+          sm100::mbar_arrive(&empty[s]);
+        }
+      }
+      // ---- the segment's sums ----
+      const int last = it - 1, rows = g.s.nn * a.G;
+      need(&o_done[last & 1], (last >> 1) & 1);
+      sm100::tc_fence_after();
+      uint32_t v[16];
+      tmem_ld<16>(tmem + lanes + kColFewO, v);
+      sm100::tmem_ld_wait();
+      const size_t row0 = g.t0 == 0 ? (static_cast<size_t>(g.b) * a.Hkv + g.h) *
+                                          (static_cast<size_t>(a.T) * a.G)
+                                    : static_cast<size_t>(blockIdx.x) * kRows;
+      float* dst = (g.t0 == 0 ? a.item_o : a.cta_o) + row0 * D + tok;
+      float mine = 0.f;  // ref of row `tok`
+#pragma unroll
+      for (int n = 0; n < FEW; ++n) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l[n] += __shfl_xor_sync(0xFFFFFFFFu, l[n], o);
+        if (lane == 0) s_top[warp * kRows + n] = l[n];
+        if (tok == n) mine = ref[n];
+        if (n < rows && tok < D) dst[n * D] = __uint_as_float(v[n]);
+      }
+      all_meet();
+      if (tok < rows) {
+        float sum = s_top[tok];
+#pragma unroll
+        for (int k = 1; k < 4; ++k) sum += s_top[k * kRows + tok];
+        (g.t0 == 0 ? a.item_ml : a.cta_ml)[row0 + tok] = make_float2(mine, sum);
+      }
+      all_meet();  // read before the next segment writes
+      sm100::tc_fence_before();  // o may be written again
     }
   } else {
     // ---- softmax: a part of a row's tokens per thread ----
@@ -963,7 +1198,7 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
   __syncthreads();
   if (warp == kMmaWarp) {
     sm100::tc_fence_after();
-    sm100::tmem_dealloc(tmem, 512);
+    sm100::tmem_dealloc(tmem, kTmemCols);
   }
 }
 
@@ -1304,7 +1539,9 @@ __global__ void __launch_bounds__(128, 2) finish_kernel(const AttnArgs a) {
 
 // ---- host side ------------------------------------------------------------------
 
-int copies_for(long long rows) { return rows <= 32 ? 4 : rows <= 64 ? 2 : 1; }
+int copies_for(long long rows) {
+  return rows <= kFewN ? 1 : rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+}
 
 struct Layout {
   size_t item_ml, item_o, cta_ml, cta_o, bytes;
@@ -1357,7 +1594,7 @@ int launch(K kern, unsigned grid, int threads, int smem, bool early, cudaStream_
   return UNO_OK;
 }
 
-template <int D, int COPIES>
+template <int D, int COPIES, int FEW = 0>
 int launch_cached(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a,
                   cudaStream_t st) {
   static std::atomic<uint64_t> attr_done{0};  // devices with the shared-memory opt-in
@@ -1365,8 +1602,8 @@ int launch_cached(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& 
   if (cudaGetDevice(&dev) != cudaSuccess) return UNO_ERR_CUDA;
   const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
   if (!bit || !(attr_done.load(std::memory_order_relaxed) & bit)) {
-    if (cudaFuncSetAttribute(cached_kernel<D, COPIES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Plan<D>::kBytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(cached_kernel<D, COPIES, FEW>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<D, FEW>::kBytes) != cudaSuccess)
       return UNO_ERR_CUDA;
     attr_done.fetch_or(bit, std::memory_order_relaxed);
   }
@@ -1376,15 +1613,18 @@ int launch_cached(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& 
   long long ctas = std::min<long long>(a.B * rts, kMaxCtas) * a.Hkv;
   ctas = std::min<long long>(ctas, kMaxCtas) * std::min<long long>(tiles, kMaxCtas);
   ctas = std::max<long long>(std::min<long long>(ctas, kMaxCtas), 1);
-  return launch(cached_kernel<D, COPIES>, static_cast<unsigned>(ctas), threads(COPIES), Plan<D>::kBytes,
-                true, st, mk, mv, a);
+  return launch(cached_kernel<D, COPIES, FEW>, static_cast<unsigned>(ctas), threads(COPIES),
+                Plan<D, FEW>::kBytes, true, st, mk, mv, a);
 }
 
 template <int D>
 int launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, bool cached,
                cudaStream_t st) {
   if (cached) {
-    const int rc = a.copies == 4   ? launch_cached<D, 4>(mk, mv, a, st)
+    const int rows = a.T * a.G;
+    const int rc = rows <= 4       ? launch_cached<D, 2, 4>(mk, mv, a, st)
+                   : rows <= kFewN ? launch_cached<D, 2, kFewN>(mk, mv, a, st)
+                   : a.copies == 4 ? launch_cached<D, 4>(mk, mv, a, st)
                    : a.copies == 2 ? launch_cached<D, 2>(mk, mv, a, st)
                                    : launch_cached<D, 1>(mk, mv, a, st);
     if (rc != UNO_OK) return rc;
