@@ -35,10 +35,18 @@
 // log2(e) + log2(v_scale), p = 2^(t - ref), and the normaliser sums p / v_scale in
 // float32. ref moves only when a tile's largest t exceeds it by 8 (then o and l
 // are rescaled and the tile's weights taken again), so the common tile is one
-// pass over the scores. With at most 64 (32) rows the lanes hold 2 (4) copies of
+// pass over the scores. With 17 to 64 (32) rows the lanes hold 2 (4) copies of
 // them, and each copy takes its half (quarter) of a tile's tokens: a warp's work
 // per tile falls with the rows, and the copies' sums are joined like those of
 // CTAs.
+//
+// Few rows. Up to 16 rows (a decode step's single tokens: the query heads of a KV
+// head) the sides are swapped: the tile's tokens are on the lanes, the rows are 16
+// columns. Keys are then the A operand as they lie, the queries' parts B in shared
+// memory; values (D x tokens) are A, the weights B, written to shared memory as
+// half. The products take an eighth of the tensor pipe's time and of the scores
+// nothing is computed twice, so the stream of codes is what is left (32 single
+// tokens of lengths 1 to 8191: 64 us against 82 with row copies).
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -58,14 +66,14 @@ namespace {
 
 constexpr int kTile = 128;     // cached tokens per unit of work
 constexpr int kRows = 128;     // rows (TMEM lanes) of a tile
-constexpr int kStages = 4;     // tiles of codes in shared memory
 constexpr int kProducers = 2;  // TMA warps, alternating tiles
 // Warps of cached_kernel: 4 parts() for the softmax (TMEM lane quarter = warp % 4, part
 // of a row's tokens = warp / 4), decoders() for the value decode (the first four of them
 // for the queries too), the producers, and two MMA issuers (scores; weighted values): a
 // thread that has issued products waits at its next barrier until they are done, so one
 // issuer would leave the tensor pipe idle between the two.
-__host__ __device__ constexpr int parts(int copies) { return copies == 1 ? 4 : 1; }
+// (`copies` 3 stands for tokens on the lanes in two parts, of the rows.)
+__host__ __device__ constexpr int parts(int copies) { return copies == 1 ? 4 : copies == 3 ? 2 : 1; }
 __host__ __device__ constexpr int decoders(int copies) { return copies == 1 ? 4 : 8; }
 constexpr int threads(int copies) {
   return 32 * (4 * parts(copies) + decoders(copies) + kProducers + 2);
@@ -73,11 +81,17 @@ constexpr int threads(int copies) {
 constexpr int kMaxCtas = 148;  // one CTA per SM
 constexpr int kMaxT = 4096;    // new tokens per sequence
 constexpr long long kWaitClocks = 2000000000ll;  // bound of every wait: about a second
-constexpr int kFewN = 16;  // columns of the products of few rows
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kStages = 4;     // tiles of codes in shared memory
 constexpr int kCachedSeqs = 512;  // sequences whose sizes a CTA keeps in shared memory
+// Up to so many rows the tokens take the TMEM lanes: the products are 16 columns wide
+// instead of 128, and the softmax has no lanes to fill. Its work grows with the rows,
+// though, a warp's 32 tokens at a time (64 sequences of 2040 to 4000 tokens, 8 KV heads;
+// us with tokens and with row copies on the lanes: 4 rows 105 and 132, 8 rows 111 and
+// 133, 16 rows 129 and 138; 48 rows 190 and 178, 68 rows 305 and 192).
+constexpr int kFewRows = 16;
+constexpr float kLog2e = 1.4426950408889634f;
 // Units that an item's start counts for, in tiles (32 single tokens of lengths 1 to
-// 8191: 94 us with 3, 86 us with 4 or 5).
+// 8191: 64 us with 2 to 5; a tree of 241 nodes over 5001: 47 us with 2, 44 with 5).
 constexpr int kLead = 5;
 constexpr float kLift = 8.f;   // log2 of how far a weight may pass 1 before its row's ref moves
 // Floor of a row's ref: a tile without a finite score leaves it there.
@@ -263,6 +277,26 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
   }
 }
 
+// R (a multiple of 4) consecutive columns.
+template <int R>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
+  if constexpr (R >= 16) {
+    tmem_ld<16>(taddr, r);
+    if constexpr (R > 16) tmem_ld_cols<R - 16>(taddr + 16, r + 16);
+  } else {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
+    if constexpr (R > 4) tmem_ld_cols<R - 4>(taddr + 4, r + 4);
+  }
+}
+template <int R>
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]));
+  if constexpr (R > 4) tmem_st_cols<R - 4>(taddr + 4, r + 4);
+}
+
 // D[tmem] (+)= A[smem desc] B[smem desc] on e4m3 codes, one thread.
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a_desc, uint64_t b_desc,
                                        uint32_t idesc, bool accumulate) {
@@ -344,18 +378,19 @@ struct Plan {
   static constexpr int kStage = 2 * kTile * D;
   static constexpr int kHalfTile = kTile * D * 2;
   static constexpr int kDecoded = kStages * kStage;
-  // (few rows) [segment parity][part][kFewN rows][D] codes; [tile parity] weights
+  // (few rows) [segment parity][part][kFewRows][D] codes; [tile parity] weights
   static constexpr int kQueries = kDecoded + 2 * kHalfTile;
-  static constexpr int kQueryPart = kFewN * D;
+  static constexpr int kQueryPart = kFewRows * D;
   static constexpr int kWeights = kQueries + (FEW ? 4 * kQueryPart : 0);
-  static constexpr int kWeightTile = kFewN * kTile * 2;
+  static constexpr int kWeightTile = kFewRows * kTile * 2;
   static constexpr int kScales = kWeights + (FEW ? 2 * kWeightTile : 0);
   static constexpr int kFactors = kScales + kStages * (kTile / 16) * 16;
-  static constexpr int kTops = kFactors + 2 * kRows * 4;  // [part][lane]
-  static constexpr int kFlags = kTops + 4 * kRows * 4;    // [tile parity][quarter][part]
+  static constexpr int kTops = kFactors + 2 * kRows * 4;  // [part][lane], or [quarter][row]
+  static constexpr int kRefs = kTops + 4 * kRows * 4;  // (few rows) [quarter][row]
+  static constexpr int kFlags = kRefs + (FEW ? 4 * kFewRows * 4 : 0);  // [tile parity][quarter][part]
   static constexpr int kBars = kFlags + 2 * 4 * 4 * 4;
   static constexpr int kBytes = kBars + (2 * kStages + 8) * 8 + 8 + 1024;  // + alignment
-  static_assert(kBytes <= 232448, "dynamic shared memory per CTA (227 KB)");
+  static_assert(kBytes + 2 * 4 * kCachedSeqs + 128 <= 232448, "dynamic shared memory per CTA (227 KB)");
 };
 
 // Row of a tile that a TMEM lane holds: with 4 copies of at most 32 rows, with 2 of
@@ -365,8 +400,8 @@ __device__ __forceinline__ int row_of_lane(int lane) {
   return lane & (kRows / COPIES - 1);
 }
 
-// FEW > 0: at most FEW rows, tokens on the lanes (COPIES is 2 then, for the warps' roles,
-// and the sums are one copy).
+// FEW > 0: at most FEW rows, tokens on the lanes (COPIES then says the warps' roles, and
+// the sums are one copy).
 template <int D, int COPIES, int FEW>
 __global__ void __launch_bounds__(threads(COPIES), 1)
     cached_kernel(const __grid_constant__ CUtensorMap map_k,
@@ -384,8 +419,8 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
   // before has been read, without its weighted values, for a softmax that is shorter
   // than the products; the next segment's queries then come late, but the epilogue of
   // the segment before takes longer still.
-  constexpr bool kOwnWeights = COPIES > 1;
-  constexpr bool kLateQueries = kOwnWeights && !FEW;
+  constexpr bool kOwnWeights = COPIES > 1 || FEW > 0;
+  constexpr bool kLateQueries = COPIES > 1 && !FEW;
   constexpr uint32_t kColO = 2 * kTile, kColQ = kColO + D, kColP = kColQ + D / 2;
   static_assert(kColQ + D <= 512 && kColP + kTile / 2 <= 512, "TMEM columns");
   constexpr uint32_t kIdescS = (1u << 4) | ((kTile >> 3) << 17) | ((kRows >> 4) << 24);
@@ -393,10 +428,10 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
       (1u << 4) | (1u << 16) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((kRows >> 4) << 24);
   // few rows: keys (tokens x D) times queries, and values (D x tokens, the values'
   // descriptor on the A side) times weights
-  constexpr uint32_t kColFewO = 2 * kFewN;
-  constexpr uint32_t kIdescFewS = (1u << 4) | ((kFewN >> 3) << 17) | ((kRows >> 4) << 24);
+  constexpr uint32_t kColFewO = 2 * kFewRows;
+  constexpr uint32_t kIdescFewS = (1u << 4) | ((kFewRows >> 3) << 17) | ((kRows >> 4) << 24);
   constexpr uint32_t kIdescFewO =
-      (1u << 4) | (1u << 15) | ((kFewN >> 3) << 17) | ((kRows >> 4) << 24);
+      (1u << 4) | (1u << 15) | ((kFewRows >> 3) << 17) | ((kRows >> 4) << 24);
   constexpr uint32_t kTmemCols = FEW ? 64 : 512;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -569,7 +604,7 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
-              mma_f8(tmem + (it & 1) * kFewN, kd + 2 * k, qd + part * (P::kQueryPart >> 4) + 2 * k,
+              mma_f8(tmem + (it & 1) * kFewRows, kd + 2 * k, qd + part * (P::kQueryPart >> 4) + 2 * k,
                      kIdescFewS, part + k > 0);
         } else {
           const uint32_t d = tmem + (it & 1) * kTile;
@@ -851,8 +886,8 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
           // weighted values. (From a segment's second tile on that has been waited for
           // above; asked again now, this tile's own could have ended a phase later.)
           if (kLateQueries ? !wait(&s_full[k2], (it >> 1) & 1)
-                          : ti == g.t0 && before >= 0 &&
-                                !wait(&o_done[before & 1], (before >> 1) & 1)) {
+                           : ti == g.t0 && before >= 0 &&
+                                 !wait(&o_done[before & 1], (before >> 1) & 1)) {
             give_up(kFaultSoftmax);
             ok = false;
             break;
@@ -862,9 +897,12 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
       }
     }
   } else if constexpr (FEW > 0) {
-    // ---- softmax of few rows: a token per thread, its weights for every row ----
-    const int tok = threadIdx.x;  // token of a tile, and TMEM lane
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    // ---- softmax of few rows: a token per thread, its weights for R of the rows ----
+    constexpr int R = FEW / PARTS;
+    static_assert(FEW % PARTS == 0 && R % 4 == 0, "rows of a part");
+    const int quarter = warp & 3, part = warp >> 2;
+    const int tok = quarter * 32 + lane;  // token of a tile, and TMEM lane
+    const uint32_t cols = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + part * R;
     int it = 0, seg = 0;
     bool ok = true;  // false: go on without waiting, the results are abandoned
     auto need = [&](uint64_t* bar, uint32_t parity) {
@@ -875,20 +913,23 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
       }
       __syncwarp();
     };
-    auto all_meet = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    // the part's warps, one per quarter, share the rows: they meet
+    auto part_meet = [&] { asm volatile("bar.sync %0, 128;" ::"r"(part + 1) : "memory"); };
+    float* const tops = s_top + part * R;  // [quarter][kFewRows]
+    // this warp's own copy of the rows' refs
+    float4* const refs =
+        reinterpret_cast<float4*>(smem + P::kRefs) + (quarter * kFewRows + part * R) / 4;
     // weights of a tile: [half of the tokens][row][64 tokens], 16-byte chunks swizzled
-    uint8_t* const wrow = smem + P::kWeights + (tok >> 6) * (P::kWeightTile / 2) + (tok & 7) * 2;
+    uint8_t* const wrow = smem + P::kWeights + (tok >> 6) * (P::kWeightTile / 2) + (tok & 7) * 2 +
+                          part * R * 128;
     const int chunk = (tok & 63) >> 3;
     Segment g;
     for (long long u = u0; next_segment(u, g); ++seg) {
       need(&q_full[seg & 1], (seg >> 1) & 1);
-      float qf[FEW], ref[FEW], l[FEW];
+      const float4* qf = reinterpret_cast<const float4*>(s_factor + (seg & 1) * kRows + part * R);
+      float l[R];
 #pragma unroll
-      for (int n = 0; n < FEW; ++n) {
-        qf[n] = s_factor[(seg & 1) * kRows + n];
-        ref[n] = kLowest;
-        l[n] = 0.f;
-      }
+      for (int n = 0; n < R; ++n) l[n] = 0.f;
       for (int ti = g.t0; ti < g.t1; ++ti, ++it) {
         const int s = it % kStages, k2 = it & 1;
         need(&full[s], (it / kStages) & 1);  // the scales
@@ -896,65 +937,85 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
         const bool in = ti * kTile + tok < g.s.len;
         need(&s_full[k2], (it >> 1) & 1);
         sm100::tc_fence_after();
-        uint32_t v[16];
-        tmem_ld<16>(tmem + lanes + k2 * kFewN, v);
+        uint32_t v[R];
+        tmem_ld_cols<R>(cols + k2 * kFewRows, v);
         sm100::tmem_ld_wait();
-        float t[FEW];
+        float t[R], top = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < FEW; ++n)
-          t[n] = in ? fmaf(__uint_as_float(v[n]), qf[n] * x.x, x.y) : -INFINITY;
+        for (int n = 0; n < R; n += 4) {
+          const float4 f = qf[n / 4], ref = refs[n / 4];
+          t[n] = in ? fmaf(__uint_as_float(v[n]), f.x * x.x, x.y) : -INFINITY;
+          t[n + 1] = in ? fmaf(__uint_as_float(v[n + 1]), f.y * x.x, x.y) : -INFINITY;
+          t[n + 2] = in ? fmaf(__uint_as_float(v[n + 2]), f.z * x.x, x.y) : -INFINITY;
+          t[n + 3] = in ? fmaf(__uint_as_float(v[n + 3]), f.w * x.x, x.y) : -INFINITY;
+          top = fmaxf(top, fmaxf(fmaxf(t[n] - ref.x, t[n + 1] - ref.y),
+                                 fmaxf(t[n + 2] - ref.z, t[n + 3] - ref.w)));
+        }
         bool move = ti == g.t0;  // the first tile sets the refs
         if (!move) {
           // they move when any token asks for it (the flags alternate with the tiles, so
           // a meeting later they may be rewritten)
-          float top = -INFINITY;
-#pragma unroll
-          for (int n = 0; n < FEW; ++n) top = fmaxf(top, t[n] - ref[n]);
           const bool ask = __any_sync(0xFFFFFFFFu, top > kLift);
-          if (lane == 0) s_flag[k2 * 4 + warp] = ask;
-          all_meet();
+          if (lane == 0) s_flag[(k2 * 4 + part) * 4 + quarter] = ask;
+          part_meet();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) move |= s_flag[k2 * 4 + k] != 0;
+          for (int k = 0; k < 4; ++k) move |= s_flag[(k2 * 4 + part) * 4 + k] != 0;
         }
         if (move) {
 #pragma unroll
-          for (int n = 0; n < FEW; ++n) {
+          for (int n = 0; n < R; ++n) {
             float mx = fmaxf(t[n], kLowest);
 #pragma unroll
             for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-            if (lane == 0) s_top[warp * kRows + n] = mx;
+            if (lane == 0) tops[quarter * kFewRows + n] = mx;
           }
-          all_meet();  // (read before the next write: a tile's flags or a segment's end lie between)
-          float al[FEW];
+          // (read before the next write: a tile's flags or a segment's end lie between)
+          part_meet();
+          // o holds the tiles before this one once the last of them has been added
+          if (ti > g.t0) need(&o_done[k2 ^ 1], ((it - 1) >> 1) & 1);
+          sm100::tc_fence_after();
 #pragma unroll
-          for (int n = 0; n < FEW; ++n) {
-            float mx = s_top[n];
+          for (int n = 0; n < R; n += 4) {
+            float mx[4], al[4];
+            const float4 old4 = refs[n / 4];
+            const float old[4] = {old4.x, old4.y, old4.z, old4.w};
 #pragma unroll
-            for (int k = 1; k < 4; ++k) mx = fmaxf(mx, s_top[k * kRows + n]);
-            const float to = ti == g.t0 || mx > ref[n] + kLift ? mx : ref[n];
-            al[n] = uno::ex2(ref[n] - to);
-            ref[n] = to;
-            l[n] *= al[n];
+            for (int e = 0; e < 4; ++e) {
+              mx[e] = tops[n + e];
+#pragma unroll
+              for (int k = 1; k < 4; ++k) mx[e] = fmaxf(mx[e], tops[k * kFewRows + n + e]);
+              if (ti > g.t0) mx[e] = mx[e] > old[e] + kLift ? mx[e] : old[e];
+              al[e] = uno::ex2(old[e] - mx[e]);
+            }
+            if (ti > g.t0) {
+              tmem_ld_cols<4>(cols + kColFewO + n, v);
+              sm100::tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                l[n + e] *= al[e];
+                v[e] = __float_as_uint(__uint_as_float(v[e]) * al[e]);
+              }
+              tmem_st_cols<4>(cols + kColFewO + n, v);
+            }
+            __syncwarp();
+            if (lane == 0) refs[n / 4] = make_float4(mx[0], mx[1], mx[2], mx[3]);
           }
-          if (ti > g.t0) {
-            // o holds the tiles before this one once the last of them has been added
-            need(&o_done[k2 ^ 1], ((it - 1) >> 1) & 1);
-            sm100::tc_fence_after();
-            tmem_ld<16>(tmem + lanes + kColFewO, v);
-            sm100::tmem_ld_wait();
-#pragma unroll
-            for (int n = 0; n < FEW; ++n) v[n] = __float_as_uint(__uint_as_float(v[n]) * al[n]);
-            tmem_st<16>(tmem + lanes + kColFewO, v);
-            sm100::tmem_st_wait();
-          }
+          sm100::tmem_st_wait();
+          __syncwarp();
         }
         if (it >= 2) need(&o_done[k2], ((it >> 1) - 1) & 1);  // the weights of tile it - 2
 #pragma unroll
-        for (int n = 0; n < FEW; ++n) {
-          const float w = uno::ex2(t[n] - ref[n]);
-          l[n] = fmaf(w, x.z, l[n]);
-          *reinterpret_cast<__half*>(wrow + k2 * P::kWeightTile + n * 128 +
-                                     ((chunk ^ (n & 7)) << 4)) = __float2half_rn(w);
+        for (int n = 0; n < R; n += 4) {
+          const float4 ref = refs[n / 4];
+          const float w[4] = {uno::ex2(t[n] - ref.x), uno::ex2(t[n + 1] - ref.y),
+                              uno::ex2(t[n + 2] - ref.z), uno::ex2(t[n + 3] - ref.w)};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            l[n + e] = fmaf(w[e], x.z, l[n + e]);
+            *reinterpret_cast<__half*>(wrow + k2 * P::kWeightTile + (n + e) * 128 +
+                                       ((chunk ^ ((part * R + n + e) & 7)) << 4)) =
+                __float2half_rn(w[e]);
+          }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         sm100::tc_fence_before();
@@ -965,33 +1026,33 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
         }
       }
       // ---- the segment's sums ----
-      const int last = it - 1, rows = g.s.nn * a.G;
+      const int last = it - 1, rows = min(max(g.s.nn * a.G - part * R, 0), R);  // of this part
       need(&o_done[last & 1], (last >> 1) & 1);
       sm100::tc_fence_after();
-      uint32_t v[16];
-      tmem_ld<16>(tmem + lanes + kColFewO, v);
+      uint32_t v[R];
+      tmem_ld_cols<R>(cols + kColFewO, v);
       sm100::tmem_ld_wait();
-      const size_t row0 = g.t0 == 0 ? (static_cast<size_t>(g.b) * a.Hkv + g.h) *
-                                          (static_cast<size_t>(a.T) * a.G)
-                                    : static_cast<size_t>(blockIdx.x) * kRows;
+      const size_t row0 = (g.t0 == 0 ? (static_cast<size_t>(g.b) * a.Hkv + g.h) *
+                                           (static_cast<size_t>(a.T) * a.G)
+                                     : static_cast<size_t>(blockIdx.x) * kRows) +
+                          part * R;
       float* dst = (g.t0 == 0 ? a.item_o : a.cta_o) + row0 * D + tok;
-      float mine = 0.f;  // ref of row `tok`
 #pragma unroll
-      for (int n = 0; n < FEW; ++n) {
+      for (int n = 0; n < R; ++n) {
 #pragma unroll
         for (int o = 16; o; o >>= 1) l[n] += __shfl_xor_sync(0xFFFFFFFFu, l[n], o);
-        if (lane == 0) s_top[warp * kRows + n] = l[n];
-        if (tok == n) mine = ref[n];
+        if (lane == 0) tops[quarter * kFewRows + n] = l[n];
         if (n < rows && tok < D) dst[n * D] = __uint_as_float(v[n]);
       }
-      all_meet();
-      if (tok < rows) {
-        float sum = s_top[tok];
+      part_meet();
+      if (tok < rows) {  // (the first quarter's lanes)
+        float sum = tops[tok];
 #pragma unroll
-        for (int k = 1; k < 4; ++k) sum += s_top[k * kRows + tok];
-        (g.t0 == 0 ? a.item_ml : a.cta_ml)[row0 + tok] = make_float2(mine, sum);
+        for (int k = 1; k < 4; ++k) sum += tops[k * kFewRows + tok];
+        (g.t0 == 0 ? a.item_ml : a.cta_ml)[row0 + tok] =
+            make_float2(reinterpret_cast<float*>(refs)[tok], sum);
       }
-      all_meet();  // read before the next segment writes
+      part_meet();  // read before the next segment writes
       sm100::tc_fence_before();  // o may be written again
     }
   } else {
@@ -1540,7 +1601,7 @@ __global__ void __launch_bounds__(128, 2) finish_kernel(const AttnArgs a) {
 // ---- host side ------------------------------------------------------------------
 
 int copies_for(long long rows) {
-  return rows <= kFewN ? 1 : rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+  return rows <= kFewRows ? 1 : rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
 }
 
 struct Layout {
@@ -1623,7 +1684,8 @@ int launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, 
   if (cached) {
     const int rows = a.T * a.G;
     const int rc = rows <= 4       ? launch_cached<D, 2, 4>(mk, mv, a, st)
-                   : rows <= kFewN ? launch_cached<D, 2, kFewN>(mk, mv, a, st)
+                   : rows <= 8     ? launch_cached<D, 3, 8>(mk, mv, a, st)
+                   : rows <= kFewRows ? launch_cached<D, 3, kFewRows>(mk, mv, a, st)
                    : a.copies == 4 ? launch_cached<D, 4>(mk, mv, a, st)
                    : a.copies == 2 ? launch_cached<D, 2>(mk, mv, a, st)
                                    : launch_cached<D, 1>(mk, mv, a, st);

@@ -384,3 +384,28 @@ def test_append_then_attend_equals_attending_with_the_rows_as_new(api):
         _check(out, q, k, v, c, lens)
         api.kv_append(c, k, v, ln, count=torch.tensor(acc, dtype=torch.int32, device=DEV))
         lens = [n + a for n, a in zip(lens, acc)]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,G", [(1, 2), (1, 3), (3, 1), (1, 5), (1, 7), (2, 4), (1, 8), (3, 3),
+                                 (1, 9), (5, 3), (4, 4), (2, 8), (1, 18)])
+def test_few_rows(api, T, G, D):
+    """Row counts around those at which the layout of a tile changes."""
+    _run(api, [900, 1, 0, 333, 128], T, 2 * G, 2, D, 32, seed=40 * T + G)
+    _run(api, [260, 5, 77], T, G, 1, D, 128, seed=50 * T + G, nodes=[0, T, max(T - 1, 1)], tree=T > 1)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,G", [(1, 4), (2, 4), (1, 8), (4, 4), (2, 16), (17, 4)])
+def test_scores_that_grow_along_the_cache(api, T, G, D):
+    """The maximum moves again and again: a row's largest scores are in its last pages."""
+    lens, width, page = [2300, 640, 129], 36, 64
+    c = _cache(api, lens, width, 1, page, D, 60 + T)
+    for b in range(len(lens)):
+        for p in range(-(-lens[b] // page)):
+            c.k_scale[int(c.page_table[b, p])] = 2.0 ** (-9 + p // 4)
+    q, k, v = _new(len(lens), T, G, 1, D, 61 + T, 0.5)
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    out = api.block_attention(q, k, v, c, ln)
+    assert api.device_fault_flags() == 0
+    _check(out, q, k, v, c, lens)
