@@ -31,9 +31,9 @@
 // the decode costs (7 clocks an element against 1).
 //
 // Softmax. A lane holds a row, and the warps of a lane quarter share the tile's
-// tokens, each with a running maximum and sum of its own. Value scales go into the exponent: t = score
-// log2(e) + log2(v_scale), p = 2^(t - ref), and the normaliser sums p / v_scale in
-// float32. ref moves only when a tile's largest t exceeds it by 8 (then o and l
+// tokens and its ref, each with a sum of its own. Value scales go into the exponent:
+// t = score log2(e) + log2(v_scale), p = 2^(t - ref), and the normaliser sums
+// p / v_scale in float32. ref moves only when a tile's largest t exceeds it by 8 (then o and l
 // are rescaled and the tile's weights taken again), so the common tile is one
 // pass over the scores. With 17 to 64 (32) rows the lanes hold 2 (4) copies of
 // them, and each copy takes its half (quarter) of a tile's tokens: a warp's work
