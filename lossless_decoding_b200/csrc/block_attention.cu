@@ -881,13 +881,15 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
           sm100::mbar_arrive(&empty[s]);
         }
         if (more && tid < 128 && ti == (kLateQueries ? g.t1 - 1 : min(g.t0 + 1, g.t1 - 1))) {
-          // The next segment's queries, once the products of those that they replace are
-          // done: this segment's with its last scores, the one before's with its last
-          // weighted values. (From a segment's second tile on that has been waited for
-          // above; asked again now, this tile's own could have ended a phase later.)
-          if (kLateQueries ? !wait(&s_full[k2], (it >> 1) & 1)
-                           : ti == g.t0 && before >= 0 &&
-                                 !wait(&o_done[before & 1], (before >> 1) & 1)) {
+          // The next segment's queries, once those of the segment before, whose factors
+          // and barrier they take, have been used by all: its last weighted values are
+          // done. (From a segment's second tile on that has been waited for above; asked
+          // again now, this tile's own could have ended a phase later.) Late queries
+          // also take the columns of this segment's, which its last scores release; that
+          // alone says nothing of the softmax warps, which after a segment of one tile may
+          // still be at the sums of the one before it.
+          if ((ti == g.t0 && before >= 0 && !wait(&o_done[before & 1], (before >> 1) & 1)) ||
+              (kLateQueries && !wait(&s_full[k2], (it >> 1) & 1))) {
             give_up(kFaultSoftmax);
             ok = false;
             break;

@@ -409,3 +409,55 @@ def test_scores_that_grow_along_the_cache(api, T, G, D):
     out = api.block_attention(q, k, v, c, ln)
     assert api.device_fault_flags() == 0
     _check(out, q, k, v, c, lens)
+
+
+def _check_whole(out, q, k, v, c, lens):
+    """As _check, for blocks of finite values: a sequence's rows and heads at once."""
+    B, T, Hq, D = q.shape
+    H, page = k.shape[2], c.k.shape[2]
+    scale = D ** -0.5
+    for b in range(B):
+        n = int(lens[b])
+        pages = c.page_table[b, :-(-n // page)].long()
+
+        def old(codes, s):  # [H, n, D]
+            x = codes[pages].double() * s[pages].double()[:, :, None, None]
+            return x.transpose(0, 1).reshape(H, -1, D)[:, :n]
+
+        K = torch.cat([old(c.k, c.k_scale), k[b].double().transpose(0, 1)], 1)
+        V = torch.cat([old(c.v, c.v_scale), v[b].double().transpose(0, 1)], 1)
+        vs = c.v_scale[pages].double().t().repeat_interleave(page, 1)[:, None, :n]
+        Q = q[b].double().view(T, H, Hq // H, D).permute(1, 0, 2, 3).reshape(H, -1, D)
+        see = torch.cat([torch.ones(T, n, dtype=torch.bool, device=DEV),
+                         _see(None, b, T)], 1).repeat_interleave(Hq // H, 0)
+        z = (Q @ K.transpose(1, 2) * scale).masked_fill(~see, -math.inf)
+        p = torch.softmax(z, 2)
+        ref = p @ V
+        got = out[b].double().view(T, H, Hq // H, D).permute(1, 0, 2, 3).reshape(H, -1, D)
+        a_old, a_new = p[..., :n] @ V[:, :n].abs(), p[..., n:] @ V[:, n:].abs()
+        mag = (Q.abs() @ K.abs().transpose(1, 2)).masked_fill(~see, 0).amax(2, keepdim=True) * scale
+        big = z.masked_fill(~see, 0).abs().amax(2, keepdim=True)
+        d = (D + 8) * 2.0 ** -24 * mag + 4 * 2.0 ** -24 * big + 2.0 ** -11 * 2.0 ** -1
+        if n:
+            d = d + 2.0 ** -17 * scale * Q.abs().amax(2, keepdim=True) * \
+                K[:, :n].abs().sum(2).amax(1)[:, None, None]
+        top = torch.cat([p[..., :n] * vs, p[..., n:]], 2).amax(2, keepdim=True)
+        tol = 2.0 ** -11 * a_old + 2.0 ** -8 * a_new + (n + T) * 2.0 ** -25 * 448 * top \
+            + 2 * d * (a_old + a_new) + 2.0 ** -8 * ref.abs() + 1e-38
+        bad = ~((got - ref).abs() <= tol)
+        assert not bad.any(), (b, float(((got - ref).abs() / tol).max()))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,G", [(1, 4), (1, 16), (5, 4), (8, 4), (9, 4), (16, 4), (17, 4)])
+def test_many_sequences_of_one_tile(api, T, G, D):
+    """A CTA goes through several items in a row that have a single tile each: the queries of
+    one may not be replaced before every warp has taken them."""
+    lens = [1 + 37 * b % 128 for b in range(200)]
+    c = _cache(api, lens, 1, 4, 128, D, seed=70 + T)
+    q, k, v = _new(200, T, 4 * G, 4, D, 71 + T)
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    out = api.block_attention(q, k, v, c, ln)
+    torch.cuda.synchronize()
+    assert api.device_fault_flags() == 0
+    _check_whole(out, q, k, v, c, lens)
