@@ -527,8 +527,9 @@ int uno_block_attention(const void* q, const void* k_new, const void* v_new, con
  * (which correct code never does) sets a bit here, abandons its work and lets
  * the kernel exit instead of hanging the GPU: bit 0 TMA producer, bit 1 MMA
  * issuer, bit 2 epilogue of the dual-path linear, bit 3 TMA producer, bit 4
- * MMA issuers, bit 5 softmax and decode warps of the block attention. This call synchronises the device, writes the
- * current flags to *flags and clears them when `clear` is non-zero.
+ * MMA issuers, bit 5 softmax and decode warps of the block attention (rows of its
+ * output that were not completed are NaN). This call synchronises the device,
+ * writes the current flags to *flags and clears them when `clear` is non-zero.
  * ------------------------------------------------------------------------ */
 int uno_device_fault_flags(int clear, unsigned int* flags);
 
@@ -541,6 +542,14 @@ int uno_device_fault_flags(int clear, unsigned int* flags);
  * and the context stays usable. (0, 0) restores normal operation. Always
  * returns UNO_OK. */
 int uno_dualpath_test_hooks(uint64_t wait_ns, uint32_t t_flag_skew);
+
+/* The same for the block attention: when query_segments is not 0, the calls that
+ * follow announce queries only for the first query_segments parts (of a sequence, KV
+ * head and row tile) of each CTA. The waits for later ones run out after about a
+ * second: the kernels set fault bits and exit normally, the rows that were not
+ * completed come out as NaN, and the context stays usable. 0 restores normal
+ * operation. Always returns UNO_OK. */
+int uno_attention_test_hook(uint32_t query_segments);
 
 #ifdef __cplusplus
 } /* extern "C" */

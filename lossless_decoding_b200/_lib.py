@@ -107,6 +107,8 @@ def _load() -> ctypes.CDLL:
     L.uno_device_fault_flags.restype = i32
     L.uno_dualpath_test_hooks.argtypes = [u64, ctypes.c_uint32]
     L.uno_dualpath_test_hooks.restype = i32
+    L.uno_attention_test_hook.argtypes = [ctypes.c_uint32]
+    L.uno_attention_test_hook.restype = i32
     return L
 
 

@@ -99,6 +99,7 @@ constexpr float kLowest = -3.0e38f;
 
 enum : unsigned { kFaultProducer = 8u, kFaultMma = 16u, kFaultSoftmax = 32u };
 __device__ unsigned int g_attn_fault;
+constexpr int kLost = -1;  // how many, of an item whose CTA had given up before it
 
 struct AttnArgs {
   const uint16_t* q;      // [B][T][Hq][D]
@@ -114,9 +115,10 @@ struct AttnArgs {
   int B, T, Hq, Hkv, G, page, width, num_pages;
   int copies;             // of the rows on the lanes: 4, 2 or 1
   float scale;            // softmax scale
+  int query_segments;     // parts of a CTA whose queries are announced (all, but in tests)
   // workspace: partial sums of parts that begin an item, [B][Hkv][copies][T G], and
   // of those that begin inside one (a CTA's first), [CTA][128 lanes]; per item
-  // [B][Hkv][row tiles] the CTAs of the latter, (first, how many)
+  // [B][Hkv][row tiles] the CTAs of the latter, (first, how many), or kLost
   int2* item_ctas;
   float2* item_ml;        // (ref, normaliser)
   float* item_o;          // [..][D]
@@ -176,6 +178,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+
+__device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7FC00000u); }
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -643,7 +647,9 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
       };
       int it = 0, seg = 0;
       Segment g;
-      for (long long u = u0; ok && next_segment(u, g); ++seg) {
+      const int rts = (a.T * a.G + kRows - 1) / kRows;
+      long long u = u0;
+      for (; ok && next_segment(u, g); ++seg) {
         if (warp == kMmaWarp && !need(&q_full[seg & 1], (seg >> 1) & 1)) break;
         if (g.t0 == 0 && warp > kMmaWarp) {
           // CTA j begins at unit floor(total j / ctas): inside the item while that is
@@ -652,7 +658,6 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
           if (g.end < g.item_end)
             n = static_cast<int>((g.item_end * s_ctas + s_total - 1) / s_total) -
                 static_cast<int>(blockIdx.x) - 1;
-          const int rts = (a.T * a.G + kRows - 1) / kRows;
           a.item_ctas[(static_cast<size_t>(g.b) * a.Hkv + g.h) * rts + g.rt] =
               make_int2(static_cast<int>(blockIdx.x) + 1, n);
         }
@@ -661,6 +666,11 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
           else values(it, j == 0);
         }
       }
+      // Given up: finish_kernel reads the entries of the items that are left all the same.
+      while (!ok && warp > kMmaWarp && next_segment(u, g))
+        if (g.t0 == 0)
+          a.item_ctas[(static_cast<size_t>(g.b) * a.Hkv + g.h) * rts + g.rt] =
+              make_int2(0, kLost);
       sm100::mma_commit(&s_end);
       if (!wait_one(&s_end, 0)) give_up(kFaultMma);
     }
@@ -774,7 +784,7 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) sm100::mbar_arrive(&q_full[seg & 1]);
+        if (lane == 0 && seg < a.query_segments) sm100::mbar_arrive(&q_full[seg & 1]);
         return;
       }
       // q 2^sh = hi + lo, its largest magnitude in [128, 256)
@@ -831,7 +841,7 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
       sm100::tmem_st_wait();
       sm100::tc_fence_before();
       __syncwarp();
-      if (lane == 0) sm100::mbar_arrive(&q_full[seg & 1]);
+      if (lane == 0 && seg < a.query_segments) sm100::mbar_arrive(&q_full[seg & 1]);
     };
     int it = 0, seg = 0;
     bool ok = true;
@@ -1027,7 +1037,8 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
           sm100::mbar_arrive(&empty[s]);
         }
       }
-      // ---- the segment's sums ----
+      // ---- the segment's sums: NaN once a wait has run out (where a segment is not complete
+      // the one for its last tile does) ----
       const int last = it - 1, rows = min(max(g.s.nn * a.G - part * R, 0), R);  // of this part
       need(&o_done[last & 1], (last >> 1) & 1);
       sm100::tc_fence_after();
@@ -1052,7 +1063,7 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
 #pragma unroll
         for (int k = 1; k < 4; ++k) sum += tops[k * kFewRows + tok];
         (g.t0 == 0 ? a.item_ml : a.cta_ml)[row0 + tok] =
-            make_float2(reinterpret_cast<float*>(refs)[tok], sum);
+            make_float2(reinterpret_cast<float*>(refs)[tok], s_abort ? quiet_nan() : sum);
       }
       part_meet();  // read before the next segment writes
       sm100::tc_fence_before();  // o may be written again
@@ -1222,7 +1233,8 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
           sm100::mbar_arrive(&empty[s]);
         }
       }
-      // ---- the segment's sums ----
+      // ---- the segment's sums: NaN once a wait has run out (where a segment is not complete
+      // the one for its last tile does) ----
       const int last = it - 1;
       need(&o_done[last & 1], (last >> 1) & 1);
       sm100::tc_fence_after();
@@ -1239,7 +1251,7 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
         if (part == 0 && valid) {
 #pragma unroll
           for (int k = 1; k < PARTS; ++k) l += s_top[k * kRows + tl];
-          (g.t0 == 0 ? a.item_ml : a.cta_ml)[row] = make_float2(ref, l);
+          (g.t0 == 0 ? a.item_ml : a.cta_ml)[row] = make_float2(ref, s_abort ? quiet_nan() : l);
         }
         meet<PARTS>(quarter);
 #pragma unroll 1
@@ -1505,10 +1517,14 @@ __global__ void __launch_bounds__(128, 2) finish_kernel(const AttnArgs a) {
 
   // ---- partial sums over the cached tokens ----
   uno::grid_dependency_wait();
+  bool lost = false;  // the cached tokens' sums: the rows come out as NaN
   if (sq.tiles > 0) {
     const int rt = r0 / kRows;
-    const int2 more = a.item_ctas[(static_cast<size_t>(b) * a.Hkv + h) *
-                                      ((a.T * a.G + kRows - 1) / kRows) + rt];
+    // kLost, or anything else that is no range of CTAs: no other part is read
+    int2 more = a.item_ctas[(static_cast<size_t>(b) * a.Hkv + h) *
+                                ((a.T * a.G + kRows - 1) / kRows) + rt];
+    lost = more.x < 1 || more.x > kMaxCtas || more.y < 0 || more.y > kMaxCtas - more.x;
+    if (lost) more = make_int2(0, 0);
     const int lanes_per_copy = kRows / a.copies;
     // adds the partial sums at rows at0 + r (r of this lane's rows) of ml and po
     auto add = [&](const float2* ml, const float* po, size_t at0, int r_off) {
@@ -1580,7 +1596,7 @@ __global__ void __launch_bounds__(128, 2) finish_kernel(const AttnArgs a) {
       }
     }
   }
-  if (sq.bad) l[0] = l[1] = __uint_as_float(0x7FC00000u);
+  if (sq.bad || lost) l[0] = l[1] = quiet_nan();
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if (rows[i] >= R) continue;
@@ -1601,6 +1617,9 @@ __global__ void __launch_bounds__(128, 2) finish_kernel(const AttnArgs a) {
 }
 
 // ---- host side ------------------------------------------------------------------
+
+// Failure-path test hook (uno_attention_test_hook); zero: normal operation.
+std::atomic<uint32_t> g_test_query_segments{0};
 
 int copies_for(long long rows) {
   return rows <= kFewRows ? 1 : rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
@@ -1726,6 +1745,11 @@ int attention_fault_flags(bool clear, unsigned* flags) {
 
 }  // namespace uno_host
 
+extern "C" int uno_attention_test_hook(uint32_t query_segments) {
+  g_test_query_segments.store(query_segments);
+  return UNO_OK;
+}
+
 extern "C" size_t uno_block_attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
   if (!sizes_ok(B, T, Hq, Hkv, D, 64, 0, 0)) return 0;
   return layout(B, T, Hq, Hkv, D).bytes;
@@ -1778,6 +1802,8 @@ extern "C" int uno_block_attention(const void* q, const void* k_new, const void*
   a.width = cached ? width : 0;
   a.num_pages = num_pages;
   a.scale = scale;
+  const uint32_t segments = g_test_query_segments.load();
+  a.query_segments = segments && segments < 0x7FFFFFFFu ? static_cast<int>(segments) : 0x7FFFFFFF;
   char* ws = static_cast<char*>(workspace);
   a.item_ctas = reinterpret_cast<int2*>(ws);
   a.item_ml = reinterpret_cast<float2*>(ws + w.item_ml);
