@@ -56,6 +56,9 @@
 #include <mutex>
 #include <type_traits>
 
+#include <sys/random.h>
+#include <unistd.h>
+
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -101,7 +104,7 @@ struct GroupArgs {
   const float* w_scale;  // [ncols] scale per output channel (int8 only)
   const float* a_scale;  // [r] scale per row of the LoRA A (int8 only)
   void* t_buf;        // T [M][r]
-  uint32_t* t_flags;  // [nT]
+  uint64_t* t_flags;  // [nT]
   float2* stats_ar;     // [M][stats_tiles] row softmax partials of y_ar (may be null)
   float2* stats_draft;  // [M][stats_tiles] the same for y_draft (may be null)
   int stats_tiles;      // column tiles of the projection: ceil(d_out / BN)
@@ -116,8 +119,8 @@ struct GemmParams {
   int r;              // adapter rank
   uint32_t idesc_t;   // instruction descriptor of the T tiles
   int t_brows;        // rows of the B box of a T-tile item (per CTA)
-  uint32_t epoch;     // value a T tile's flag takes once T is stored
-  uint32_t t_wait_epoch;  // value a producer waits for on a T flag (== epoch, except
+  uint64_t epoch;     // value a T tile's flag takes once T is stored
+  uint64_t t_wait_epoch;  // value a producer waits for on a T flag (== epoch, except
                           // under the failure-path test hook: a value no tile writes)
   uint64_t wait_ns;   // limit of every bounded wait (1 s; shorter under the test hook)
   int main_tiles;     // main tiles over all projections
@@ -129,7 +132,7 @@ struct GemmParams {
   int split_start;    // first split unit (== total units when nothing is split)
   int split_k;        // pieces per split tile (1: no split)
   float* part_buf;    // [n_split][split_k - 1][CTAs per tile][BN / 4][128][4] fp32
-  uint32_t* part_flags;  // [n_split][split_k - 1]
+  uint64_t* part_flags;  // [n_split][split_k - 1]
   size_t part_capacity;  // bytes available at part_buf (host side: decides the split)
   const uint8_t* gate;   // [M] per-row adapter gate (0: AR only), or null (all on)
   const float* x_scale;  // [M] scale per row of x (int8 only)
@@ -316,14 +319,14 @@ __device__ __forceinline__ float stored_value(float v) {
   else return v;
 }
 
-__device__ __forceinline__ uint32_t ld_acquire_u32(const uint32_t* p) {
-  uint32_t v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+__device__ __forceinline__ uint64_t ld_acquire_u64(const uint64_t* p) {
+  uint64_t v;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
   return v;
 }
 
-__device__ __forceinline__ void st_release_u32(uint32_t* p, uint32_t v) {
-  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+__device__ __forceinline__ void st_release_u64(uint64_t* p, uint64_t v) {
+  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
 }
 
 __device__ __forceinline__ void fence_proxy_async_global() {
@@ -448,12 +451,12 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
 }
 
 // Bounded wait until *flag == epoch.
-__device__ bool wait_flag(const uint32_t* flag, uint32_t epoch, uint64_t limit_ns) {
-  if (ld_acquire_u32(flag) == epoch) return true;
+__device__ bool wait_flag(const uint64_t* flag, uint64_t epoch, uint64_t limit_ns) {
+  if (ld_acquire_u64(flag) == epoch) return true;
   const uint64_t t0 = sm100::globaltimer_ns();
   for (;;) {
     __nanosleep(64);
-    if (ld_acquire_u32(flag) == epoch) return true;
+    if (ld_acquire_u64(flag) == epoch) return true;
     if (sm100::globaltimer_ns() - t0 > limit_ns) return false;
   }
 }
@@ -757,7 +760,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           if (t_ready != key) {
             // T must be stored before its TMA load: wait for the T tile(s)
             bool ready = true;
-            const uint32_t* fl = p.g[owner.g].t_flags;
+            const uint64_t* fl = p.g[owner.g].t_flags;
             if constexpr (SWAP) {
               for (int t = 0; t < p.nT && ready; ++t)
                 ready = wait_flag(fl + t, p.t_wait_epoch, p.wait_ns);
@@ -1326,7 +1329,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           if (warp == 0 && leader) {
             if (wait_cl(t_stored, li & 1, p.wait_ns)) {
               fence_proxy_async_global();
-              st_release_u32(p.g[gi].t_flags + x.tt, p.epoch);
+              st_release_u64(p.g[gi].t_flags + x.tt, p.epoch);
             } else {
               set_fault(kFaultEpilogue, &abort_flag);
             }
@@ -1349,7 +1352,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           // three times a whole one)
           return p.part_buf + sl * (static_cast<size_t>(kBM) * BN) + static_cast<size_t>(rr) * 4;
         };
-        uint32_t* pflags = p.part_flags + static_cast<size_t>(x.sidx) * (p.split_k - 1);
+        uint64_t* pflags = p.part_flags + static_cast<size_t>(x.sidx) * (p.split_k - 1);
         if (x.piece > 0) {
           float* dst = slot(x.piece);
           for (int c = 0; c < BN; c += 32) {
@@ -1368,7 +1371,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             arrive_leader(t_stored);  // this CTA's T tiles used phases 0 .. nt_mine-1
             if (warp == 0 && leader) {
               if (wait_cl(t_stored, nt_mine & 1, p.wait_ns))
-                st_release_u32(pflags + (x.piece - 1), p.epoch);
+                st_release_u64(pflags + (x.piece - 1), p.epoch);
               else
                 set_fault(kFaultEpilogue, &abort_flag);
             }
@@ -1572,26 +1575,36 @@ int sm_count() {
   return n;
 }
 
-// A fresh value per call for the T-tile flags. Seeded from the clock so that
-// a workspace left over from another process is not mistaken for this call's.
 // Failure-path test hook (uno_dualpath_test_hooks): a shorter limit for every
 // bounded wait, and a skew that makes producers wait for a T-flag value no
 // tile writes. Zero: normal operation.
 std::atomic<uint64_t> g_test_wait_ns{0};
 std::atomic<uint32_t> g_test_t_skew{0};
 
-uint32_t next_epoch() {
-  static std::atomic<uint32_t> counter{0};
-  static std::once_flag once;
-  std::call_once(once, [] {
-    const auto now = std::chrono::high_resolution_clock::now().time_since_epoch().count();
-    counter.store(static_cast<uint32_t>(now) * 2654435761u);
-  });
-  uint32_t e;
+// The call's value of the T-tile and piece flags. A workspace may hold anything when a
+// call begins (flags of other calls, partial sums, another program's tensors), and
+// nothing clears its flags outside stream capture: a word that happened to equal
+// the value would pass for a tile that is not there yet. So it is 64 bits, from a
+// bijection of a counter that starts at random (splitmix64: Steele, Lea, Flood,
+// OOPSLA 2014): no two calls of a process share one, none can be told from
+// those before it, and any given word is it with probability 2^-64.
+uint64_t next_epoch() {
+  static std::atomic<uint64_t> counter{[] {
+    uint64_t seed = 0;
+    if (getrandom(&seed, sizeof(seed), GRND_NONBLOCK) != static_cast<ssize_t>(sizeof(seed)))
+      seed = static_cast<uint64_t>(
+                 std::chrono::high_resolution_clock::now().time_since_epoch().count()) ^
+             (static_cast<uint64_t>(getpid()) << 40) ^ reinterpret_cast<uintptr_t>(&seed);
+    return seed;
+  }()};
+  uint64_t z;
   do {
-    e = counter.fetch_add(1) + 1;
-  } while (e == 0);
-  return e;
+    z = counter.fetch_add(0x9E3779B97F4A7C15ull);
+    z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+    z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+    z ^= z >> 31;
+  } while (z == 0);  // 0 is a cleared flag
+  return z;
 }
 
 int bn_for(int rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
@@ -1662,12 +1675,12 @@ int launch_dual(const DualMaps& maps, const GemmParams& p, cudaStream_t st) {
     while (k > 1 && p.kb_total < 2 * k) --k;
     const size_t per_slot = static_cast<size_t>(PAIR ? 2 : 1) * kBM * BN * sizeof(float);
     const size_t slots = static_cast<size_t>(rem) * (k - 1);
-    const size_t need = slots * per_slot + align256(slots * sizeof(uint32_t));
+    const size_t need = slots * per_slot + align256(slots * sizeof(uint64_t));
     if (k >= 3 && units0 - rem >= static_cast<long long>(p.nT) * p.ngroups &&
         need <= p.part_capacity) {
       q.split_k = k;
       q.split_start = static_cast<int>(units0 - rem);
-      q.part_flags = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(p.part_buf) +
+      q.part_flags = reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(p.part_buf) +
                                                  slots * per_slot);
       tiles = units0 - rem + rem * k;
     }
@@ -1753,11 +1766,11 @@ Plan make_plan(int M, int d_in, int r, int dtype) {
   // with M > 256 a CTA pair computes 256-row tiles, so one T tile per 256 rows
   pl.nT = pl.swap ? (r + kBM - 1) / kBM : (M + 2 * kBM - 1) / (2 * kBM);
   pl.t_bytes = align256(static_cast<size_t>(M) * r * t_esize);
-  pl.flag_bytes = align256(static_cast<size_t>(pl.nT) * sizeof(uint32_t));
+  pl.flag_bytes = align256(static_cast<size_t>(pl.nT) * sizeof(uint64_t));
   const int bn = pl.swap ? bn_for(M) : 256;
   const size_t per_slot = static_cast<size_t>(pl.swap ? 1 : 2) * kBM * bn * sizeof(float);
   const size_t slots = static_cast<size_t>(pl.swap ? kSizingSms : kSizingSms / 2) - 1;
-  pl.part_bytes = slots * per_slot + align256(slots * sizeof(uint32_t));
+  pl.part_bytes = slots * per_slot + align256(slots * sizeof(uint64_t));
   return pl;
 }
 
@@ -1817,7 +1830,7 @@ int run_dualpath(int n, const void* x, const void* const* W, const void* const* 
     // (swapped layout: each CTA accumulates over all of its tiles)
     a.stats_tiles = pl.swap ? kSizingSms : (d_out[g] + 255) / 256;
     a.t_buf = ws;
-    a.t_flags = reinterpret_cast<uint32_t*>(ws + pl.t_bytes);
+    a.t_flags = reinterpret_cast<uint64_t*>(ws + pl.t_bytes);
     ws += pl.t_bytes + pl.flag_bytes;
     if (pl.swap) {
       a.tiles_a = (d_out[g] + kBM - 1) / kBM;

@@ -192,3 +192,36 @@ def test_two_streams_and_captured_graphs(api):
         for w, o in zip(want, outs):
             assert torch.equal(w[0], o[0]) and torch.equal(w[1], o[1])
     assert api.device_fault_flags() == 0
+
+
+@pytest.mark.parametrize("M,d_in,d_out,r", [(1, 4096, 1024, 128), (40, 1024, 512, 32),
+                                            (1088, 1024, 4096, 128), (300, 256, 256, 64)])
+def test_whatever_the_workspace_holds(api, M, d_in, d_out, r):
+    """Its flags may hold what a caller can guess of the next call's from those of the last:
+    with all operands 0 the flags are the only words that a call leaves that are not."""
+    from lossless_decoding_b200._lib import lib
+    d = _inputs(M, d_in, d_out, r, seed=M)
+    want = api.dualpath_linear_int8(**d)
+    zero = {k: torch.zeros_like(v) if torch.is_tensor(v) else v for k, v in d.items()}
+    need = int(lib.uno_dualpath_int8_workspace_bytes(M, d_in, d_out, r))
+    ws = torch.zeros((need + 7) // 8, dtype=torch.int64, device=DEV)
+    w32 = ws.view(torch.int32)
+    for guess in ("the same", "32-bit words", "64-bit words"):
+        ws.zero_()
+        api.dualpath_linear_int8(**zero, workspace=ws)
+        at32, at64 = w32 != 0, ws != 0
+        assert at32.any()
+        if guess == "32-bit words":
+            w32 += 1
+        elif guess == "64-bit words":
+            ws += 1
+        # everything else: large halves of floats, and large integers
+        if guess == "64-bit words":
+            ws[~at64] = 0x7F007F007F007F00
+        else:
+            w32[~at32] = 0x7F007F00
+        got = api.dualpath_linear_int8(**d, workspace=ws)
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b), guess
+    assert api.device_fault_flags() == 0
