@@ -904,6 +904,8 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
             ok = false;
             break;
           }
+          // the products that read the columns come before the stores that replace them
+          sm100::tc_fence_after();
           stage_queries(next, seg + 1);
         }
       }
