@@ -1611,13 +1611,14 @@ int bn_for(int rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Clusters of two that can be resident at once (cached per device).
-template <typename K>
-int max_pairs(K kern, int bytes) {
-  static int cached[64];
+// Clusters of two of a kernel that can be resident at once (cached per kernel and device:
+// the kernels differ in shared memory, and share a type).
+template <auto kern>
+int max_pairs(int bytes) {
+  static std::atomic<int> cached[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count() / 2;
-  if (cached[dev]) return cached[dev];
+  if (const int known = cached[dev].load(std::memory_order_relaxed)) return known;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(sm_count() & ~1));
   cfg.blockDim = dim3(kGemmThreads);
@@ -1634,14 +1635,14 @@ int max_pairs(K kern, int bytes) {
     (void)cudaGetLastError();
     n = sm_count() / 2;
   }
-  cached[dev] = n;
+  cached[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
 template <typename T, typename Y, int BN, bool SWAP, bool PAIR>
 int launch_dual(const DualMaps& maps, const GemmParams& p, cudaStream_t st) {
   constexpr int bytes = smem_bytes<BN, PAIR, T, Y>();
-  auto kern = dual_kernel<T, Y, BN, SWAP, PAIR>;
+  constexpr auto kern = dual_kernel<T, Y, BN, SWAP, PAIR>;
   static std::atomic<uint64_t> attr_done{0};  // devices with the shared-memory opt-in
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return UNO_ERR_CUDA;
@@ -1653,7 +1654,8 @@ int launch_dual(const DualMaps& maps, const GemmParams& p, cudaStream_t st) {
     attr_done.fetch_or(bit, std::memory_order_relaxed);
   }
   const long long units0 = static_cast<long long>(p.nT) * p.ngroups + p.main_tiles;
-  long long resident = PAIR ? max_pairs(kern, bytes) : sm_count();
+  long long resident = sm_count();
+  if constexpr (PAIR) resident = max_pairs<dual_kernel<T, Y, BN, SWAP, PAIR>>(bytes);
   // the swapped layout's row statistics have one slot per CTA: the launch
   // (and the split plan below, which assumes every CTA is resident) uses at
   // most that many CTAs
