@@ -63,6 +63,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include "dual_units.h"
 #include "sm100.cuh"
 #include "uno.h"
 #include "uno_device.cuh"
@@ -83,7 +84,7 @@ constexpr int kInsert = 6;         // main K-blocks of the next tile before an a
 // (1088 x 4096 -> 12288: 74 us with 6, 71 with 12, 68 with 18, 67 with 24)
 constexpr int kInsertI8 = 24;
 constexpr int kPrefetch = 8;       // K-blocks of L2 prefetch ahead of the weight loads
-constexpr int kMaxSplit = 4;       // K-pieces of a split tile, at most
+using dual_units::kMaxSplit;       // K-pieces of a split tile, at most
 constexpr uint64_t kWaitNs = 1000000000ull;  // default limit of every bounded wait
 
 enum : unsigned { kFaultProducer = 1u, kFaultMma = 2u, kFaultEpilogue = 4u };
@@ -125,8 +126,8 @@ struct GemmParams {
   uint64_t wait_ns;   // limit of every bounded wait (1 s; shorter under the test hook)
   int main_tiles;     // main tiles over all projections
   // The last, partial round of main tiles may be split along K so that it
-  // fills the GPU: units [split_start, split_start + n_split * split_k) are
-  // piece (j % split_k) of main tile (split_start - nT * ngroups + j / split_k).
+  // fills the GPU: units [split_start, split_start + n_split * split_k) are pieces of
+  // the main tiles from split_start - nT * ngroups on (dual_units::split_unit).
   // Piece 0 adds the fp32 partials of the other pieces (part_buf slots,
   // published through part_flags) before its epilogue.
   int split_start;    // first split unit (== total units when nothing is split)
@@ -616,9 +617,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     } else {
       int u = t - nt_all;
       if (t >= p.split_start) {
-        const int j = t - p.split_start;
-        x.sidx = j / p.split_k;
-        x.piece = j - x.sidx * p.split_k;
+        const dual_units::SplitUnit su = dual_units::split_unit(t - p.split_start, p.split_k);
+        x.sidx = su.tile;
+        x.piece = su.piece;
         x.kb0 = x.piece * nkb / p.split_k;  // balanced: no piece is empty (nkb >= split_k)
         x.kb1 = (x.piece + 1) * nkb / p.split_k;
         u = p.split_start - nt_all + x.sidx;
@@ -1661,31 +1662,23 @@ int launch_dual(const DualMaps& maps, const GemmParams& p, cudaStream_t st) {
   // most that many CTAs
   if (SWAP && (p.g[0].stats_ar || p.g[0].stats_draft) && resident > p.g[0].stats_tiles)
     resident = p.g[0].stats_tiles;
-  // Split the last, partial round of main tiles along K over the CTAs (or
-  // pairs) it would leave idle: 3 or 4 pieces, each of at least 2 K-blocks.
-  // (Two pieces do not pay for the hand-off of the fp32 partial: measured on
-  // 256 x 256 tiles, the round got slower.)
+  // (int8: also when all tiles together would leave most SMs idle; its sums are exact,
+  // so the pieces change no result)
+  const long long t_units = static_cast<long long>(p.nT) * p.ngroups;
+  const size_t per_slot = static_cast<size_t>(PAIR ? 2 : 1) * kBM * BN * sizeof(float);
+  const dual_units::Split sp =
+      dual_units::split_plan(t_units, p.main_tiles, resident, p.kb_total, sizeof(T) == 1);
+  const size_t slots = static_cast<size_t>(sp.tiles) * (sp.k - 1);
   GemmParams q = p;
   q.split_start = static_cast<int>(units0);
   q.split_k = 1;
   long long tiles = units0;
-  // (int8: also when all tiles together would leave most SMs idle; its sums are exact,
-  // so the pieces change no result)
-  if (units0 > resident || (sizeof(T) == 1 && 3 * units0 <= resident)) {
-    const long long rem = units0 > resident ? units0 % resident : p.main_tiles;
-    int k = rem > 0 ? static_cast<int>(std::min<long long>(kMaxSplit, resident / rem)) : 1;
-    while (k > 1 && p.kb_total < 2 * k) --k;
-    const size_t per_slot = static_cast<size_t>(PAIR ? 2 : 1) * kBM * BN * sizeof(float);
-    const size_t slots = static_cast<size_t>(rem) * (k - 1);
-    const size_t need = slots * per_slot + align256(slots * sizeof(uint64_t));
-    if (k >= 3 && units0 - rem >= static_cast<long long>(p.nT) * p.ngroups &&
-        need <= p.part_capacity) {
-      q.split_k = k;
-      q.split_start = static_cast<int>(units0 - rem);
-      q.part_flags = reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(p.part_buf) +
-                                                 slots * per_slot);
-      tiles = units0 - rem + rem * k;
-    }
+  if (sp.k > 1 && slots * per_slot + align256(slots * sizeof(uint64_t)) <= p.part_capacity) {
+    q.split_k = sp.k;
+    q.split_start = static_cast<int>(units0 - sp.tiles);
+    q.part_flags = reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(p.part_buf) +
+                                               slots * per_slot);
+    tiles = units0 - sp.tiles + static_cast<long long>(sp.tiles) * sp.k;
   }
   if constexpr (PAIR) {
     long long pairs = resident;
