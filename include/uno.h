@@ -392,7 +392,9 @@ int uno_tree_verify(const void* p_logits, const int32_t* node_token, const int32
  *   y = h / sqrt(mean(h^2) + eps) * w     float32, from the rounded h
  *   scale = max|y| / 127,  q = y / scale rounded to nearest even, |q| <= 127
  * uno_quantize_rows is the last line alone, for inputs that no norm writes
- * (attention outputs, MLP activations). A row of zeros has scale 0 and q 0. A
+ * (attention outputs, MLP activations). Its q is exact for bf16 rows; for f32 rows
+ * and after a norm y / scale is float32, so that values within 2^-22 of themselves of a
+ * half may go to either side of it (half of the row's largest goes to 64). A row of zeros has scale 0 and q 0. A
  * row with an infinity or NaN (in the input, in h w, or because its sum of
  * squares passes float32) has scale NaN and q 0, and so has, with eps = 0, a
  * row whose squares are all 0 in float32.

@@ -11,7 +11,7 @@
 // one fma onto 1.5 * 2^23, whose low byte is then the integer: 82 us against
 // 139 us of 8192 x 12288 with conversions to int). The row factor
 // r = rsqrt(..) scales every |h w| alike, so max|y| = r max|h w| and
-// q = rint(h w * 127 / max|h w|): the sum of squares and the maximum are one
+// q = rint(h w * (127 / max|h w|)): the sum of squares and the maximum are one
 // block reduction, not two with the row read again between them.
 //
 // Maxima keep NaN and are compared as bit patterns across threads (NaN above
@@ -131,11 +131,26 @@ __device__ __forceinline__ void add_rows(float* f, const float* r, T* h) {
   }
 }
 
+// Onto it a float32 rounds to an integer, to nearest even, that is then its low bits.
+constexpr float kRound = 12582912.f;  // 1.5 * 2^23
+constexpr float kLift = 0x1p64f;      // of rows whose 127 / max passes float32 (maxima below 2^-121)
+
+// 127 / max of a row, infinite where it passes float32. Rounded up: a value of half the
+// maximum is 63.5 steps and has to become 64 (nearest even), which it does if the product
+// is 63.5 or a little more, and does not (for about half of all maxima) if it is a
+// little less. Of bfloat16 rows every other value is right too: 127 x / max lies on a half,
+// then 127 / max is exact, or at least 2^-17 x from one, 2^6 times the quotient's error.
+__device__ __forceinline__ float steps_per_unit(float amax) {
+  const float inv = 127.f / amax;
+  // one step up where it is below the quotient (the remainder's sign is exact)
+  return __uint_as_float(__float_as_uint(inv) + (fmaf(inv, amax, -127.f) < 0.f));
+}
+
 // One row per group of `warps` warps (rows_per_cta groups in a CTA; a group
 // of one warp needs no shared memory). Each thread holds ITER pieces of V
 // elements, a group's pieces interleaved so that its loads are coalesced.
 template <typename T, int V, int ITER, bool NORM>
-__global__ void __launch_bounds__(1024) row_quant_kernel(const RowArgs a, int warps) {
+__global__ void __launch_bounds__(1024, 1) row_quant_kernel(const RowArgs a, int warps) {
   __shared__ float s_sum[32];
   __shared__ uint32_t s_max[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -225,8 +240,7 @@ __global__ void __launch_bounds__(1024) row_quant_kernel(const RowArgs a, int wa
   if (!a.q) return;
   const float amax = __uint_as_float(top);
   const bool bad = top >= 0x7F800000u || !(sum < INFINITY) || !(rstd < INFINITY);
-  const float inv = bad ? 0.f : 127.f / amax;
-  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: an integer added to it stays in the low bits
+  const float inv = bad ? 0.f : steps_per_unit(amax);
   int8_t* dst = a.q + at + tid * V;
   if (inv < INFINITY) {
 #pragma unroll
@@ -238,7 +252,8 @@ __global__ void __launch_bounds__(1024) row_quant_kernel(const RowArgs a, int wa
         q[k] = bad ? 0u : __float_as_uint(fmaf(f[i][k], inv, kRound));
       store_q<V>(dst + i * step, q);
     }
-  } else {  // amax = 0, or below 127 / FLT_MAX: divide instead
+  } else {  // amax = 0, or lifted
+    const float lifted = amax > 0.f ? steps_per_unit(amax * kLift) : 0.f;
 #pragma unroll 1
     for (int i = 0; i < ITER; ++i) {
       if (tid * V + i * step >= a.d) break;
@@ -249,7 +264,7 @@ __global__ void __launch_bounds__(1024) row_quant_kernel(const RowArgs a, int wa
 #pragma unroll
         for (int j = 0; j < ITER; ++j)
           if (j == i) v = f[j][k];
-        q[k] = __float_as_uint((amax > 0.f ? v / amax * 127.f : 0.f) + kRound);
+        q[k] = __float_as_uint(fmaf(v * kLift, lifted, kRound));
       }
       store_q<V>(dst + i * step, q);
     }
@@ -308,11 +323,8 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) quant_bf16_kernel(con
                           lane < static_cast<int>(blockDim.x) / 32 ? s_max[lane] : 0u);
   const float amax = uno::bf16_bits_to_float(top);
   const bool bad = top >= 0x7F80u;
-  // (below 2^-121 127 / amax passes float32: such rows are lifted by 2^64 first)
-  const bool tiny = top < 0x0300u;
-  const float inv = bad || top == 0 ? 0.f : tiny ? 127.f / (amax * 0x1p64f) : 127.f / amax;
-  const float lift = tiny ? 0x1p64f : 1.f;
-  constexpr float kRound = 12582912.f;
+  const bool tiny = amax < 0x1p-120f;
+  const float inv = bad || top == 0 ? 0.f : steps_per_unit(tiny ? amax * kLift : amax);
   int8_t* dst = a.q + at;
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
@@ -322,7 +334,7 @@ __global__ void __launch_bounds__(THREADS, 2048 / THREADS) quant_bf16_kernel(con
     uint32_t q[8];
     if (tiny) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] *= lift;
+      for (int k = 0; k < 8; ++k) f[k] *= kLift;
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k)

@@ -195,3 +195,38 @@ def test_norm_without_eps_of_rows_whose_squares_vanish(api, dtype):
     assert int(r.q[1:3].abs().max()) == 0
     _, y, scale = rms_norm(x[3:], w, 0.0)
     _check_q(r.q[3:], r.scale[3:], y, scale)
+
+
+# (M, d) of each way in which rows are taken: element by element, in 16-byte pieces with one,
+# two and four to a thread, packed
+WAYS = [(128, 41), (128, 8193), (128, 64), (256, 4096), (384, 4096), (384, 16392)]
+
+
+@pytest.mark.parametrize("e", [0, -40, 60, -119, -120, -121, -125])
+@pytest.mark.parametrize("M,d", WAYS)
+def test_bfloat16_rows_are_rounded_exactly(api, M, d, e):
+    """127 x / max in 64 bits is exact where it is a half and at least 2^-17 x from one
+    elsewhere. Each mantissa of the maximum; half of it is 63.5 steps: 64, to the even side."""
+    g = torch.Generator().manual_seed(M + d + e)
+    top = (1 + torch.arange(M) % 128 / 128).double() * 2.0 ** e
+    x = (torch.randn(M, d, generator=g).clamp(-3, 3).double() / 3 * top[:, None]).bfloat16()
+    x[:, 0], x[:, 1], x[:, d - 1], x[:, d // 2] = top, -top / 2, top / 2, -top / 4
+    assert torch.equal(x.double().abs().amax(1), top)
+    q, _ = api.quantize_rows(x.to(DEV))
+    want = torch.round(x.double() * 127 / top[:, None])
+    assert torch.all(want[:, 1] == -64) and torch.all(want[:, d - 1] == 64)
+    assert torch.equal(q.cpu().double(), want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,d", WAYS)
+def test_half_of_the_maximum_is_64_steps(api, M, d, dtype):
+    g = torch.Generator().manual_seed(M + d)
+    x = (torch.randn(M, d, generator=g) / 16).clamp(-0.9, 0.9).to(DT[dtype])
+    top = (1 + torch.rand(M, generator=g)).to(DT[dtype])
+    x[:, 0], x[:, 1], x[:, d - 1] = top, -top / 2, top / 2
+    w = torch.ones(d, dtype=DT[dtype], device=DEV)
+    for q in (api.quantize_rows(x.to(DEV))[0], api.rms_norm(x.to(DEV), w, 1e-6).q):
+        q = q.cpu()
+        assert torch.all(q[:, 0] == 127) and torch.all(q[:, 1] == -64)
+        assert torch.all(q[:, d - 1] == 64)
