@@ -490,9 +490,12 @@ int uno_kv_append(const void* k_new, const void* v_new, const int32_t* start,
  *   out = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale q . k_j)
  * over all cached positions j < lens[b] and the new tokens that i sees: j <= i,
  * or with `parent` i itself and its chain of parents. T = 1 is plain decode.
- * Float32 softmax and sums; cached values are code * scale as uno_kv_append
- * writes them (any scales >= 0; value scales outside [2^-60, 2^60] count as the
- * nearer of the two), new ones the bf16 rows.
+ * Scores, softmax statistics and sums are float32. The weights that multiply values
+ * have fewer bits: of cached tokens w_j * (value scale) as a half, off by at most 2^-11
+ * of itself, or 2^-34 of the row's largest where that is more (below 2^-23 of it); of new
+ * tokens as bfloat16, off by at most 2^-8 of itself. Cached values are code * scale as
+ * uno_kv_append writes them (any scales >= 0; value scales outside [2^-60, 2^60] count
+ * as the nearer of the two), new ones the bf16 rows.
  *
  * q, out       [B, T, Hq, D] bf16;  k_new, v_new [B, T, Hkv, D] bf16
  * lens         [B] int32 cached tokens; one outside [0, width * page] makes the

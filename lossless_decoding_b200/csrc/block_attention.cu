@@ -25,7 +25,7 @@
 // (bfloat16's 8 bits are two signed 4-bit halves; 2^s brings the row's largest
 // into [128, 256), and what e4m3's smallest step 2^-9 drops is below 2^-18 of it).
 // Weighted values: kind::f16, weights rounded to half (2^-11) as the A operand in
-// TMEM over the scores they came from, values decoded to half in shared memory by
+// TMEM over the scores they came from (kHead says how they are scaled), values decoded to half in shared memory by
 // warps of their own (exact: e4m3 is a subset). With weights in e4m3 parts
 // the decode would go, but splitting a weight costs the softmax warps more than
 // the decode costs (7 clocks an element against 1).
@@ -33,8 +33,8 @@
 // Softmax. A lane holds a row, and the warps of a lane quarter share the tile's
 // tokens and its ref, each with a sum of its own. Value scales go into the exponent:
 // t = score log2(e) + log2(v_scale), p = 2^(t - ref), and the normaliser sums
-// p / v_scale in float32. ref moves only when a tile's largest t exceeds it by 8 (then o and l
-// are rescaled and the tile's weights taken again), so the common tile is one
+// p / v_scale in float32. ref moves only when a tile's largest t exceeds it by kTop (then o and
+// l are rescaled and the tile's weights taken again), so the common tile is one
 // pass over the scores. With 17 to 64 (32) rows the lanes hold 2 (4) copies of
 // them, and each copy takes its half (quarter) of a tile's tokens: a warp's work
 // per tile falls with the rows, and the copies' sums are joined like those of
@@ -93,7 +93,14 @@ constexpr float kLog2e = 1.4426950408889634f;
 // Units that an item's start counts for, in tiles (32 single tokens of lengths 1 to
 // 8191: 64 us with 2 to 5; a tree of 241 nodes over 5001: 47 us with 2, 44 with 5).
 constexpr int kLead = 5;
-constexpr float kLift = 8.f;   // log2 of how far a weight may pass 1 before its row's ref moves
+// A row's weights are scaled so that the largest when its ref is set is 2^kHead, and may grow
+// to 2^kTop (half ends just below 2^16) before the ref moves. The head is for long
+// caches that one token dominates: half keeps its 11 bits down to 2^-14, so down to 2^-23 of
+// the largest weight, and is off by 2^-34 of it below. (With the largest at 1, each of 131072
+// tokens that share 1% was 1.3 of half's smallest steps, and a quarter of their sum was lost.)
+// The rest of half's range is for the maxima of later tiles: 64 sequences of 17 rows take
+// 182 us with heads of 7 to 9, 188 with 10, 213 with 11 and a top of 15.
+constexpr float kHead = 9.f, kTop = 15.9f;
 // Floor of a row's ref: a tile without a finite score leaves it there.
 constexpr float kLowest = -3.0e38f;
 
@@ -969,7 +976,7 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
         if (!move) {
           // they move when any token asks for it (the flags alternate with the tiles, so
           // a meeting later they may be rewritten)
-          const bool ask = __any_sync(0xFFFFFFFFu, top > kLift);
+          const bool ask = __any_sync(0xFFFFFFFFu, top > kTop);
           if (lane == 0) s_flag[(k2 * 4 + part) * 4 + quarter] = ask;
           part_meet();
 #pragma unroll
@@ -998,7 +1005,7 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
               mx[e] = tops[n + e];
 #pragma unroll
               for (int k = 1; k < 4; ++k) mx[e] = fmaxf(mx[e], tops[k * kFewRows + n + e]);
-              if (ti > g.t0) mx[e] = mx[e] > old[e] + kLift ? mx[e] : old[e];
+              mx[e] = ti == g.t0 || mx[e] > old[e] + kTop ? mx[e] - kHead : old[e];
               al[e] = uno::ex2(old[e] - mx[e]);
             }
             if (ti > g.t0) {
@@ -1182,9 +1189,9 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
                 meet<PARTS>(quarter);  // read before a next move writes
               }
               if (ti == g.t0) {
-                ref = mx;
+                ref = mx - kHead;
               } else {
-                const float to = mx > ref + kLift ? mx : ref;
+                const float to = mx > ref + kTop ? mx - kHead : ref;
                 const float al = uno::ex2(ref - to);
                 ref = to;
                 l *= al;
@@ -1205,7 +1212,7 @@ __global__ void __launch_bounds__(threads(COPIES), 1)
             }
             if (left >= HC) pass(std::true_type{});
             else pass(std::false_type{});
-            const bool ask = !move && __any_sync(0xFFFFFFFFu, top > kLift);
+            const bool ask = !move && __any_sync(0xFFFFFFFFu, top > kTop);
             if (PARTS > 1 && lane == 0) s_flag[(k2 * 4 + quarter) * 4 + part] = ask;
             meet<PARTS>(quarter);  // all parts have read the scores that the weights overwrite
             if (move) break;

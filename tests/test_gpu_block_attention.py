@@ -461,3 +461,44 @@ def test_many_sequences_of_one_tile(api, T, G, D):
     torch.cuda.synchronize()
     assert api.device_fault_flags() == 0
     _check_whole(out, q, k, v, c, lens)
+
+
+@pytest.mark.parametrize("T,G,D", [(1, 3, 64), (1, 8, 128), (2, 8, 64), (5, 4, 128),
+                                   (10, 4, 64), (20, 4, 128)])
+@pytest.mark.parametrize("n,at", [(100000, 0), (131072, 131071), (262145, 7)])
+def test_a_dominating_token_of_value_zero(api, T, G, D, n, at):
+    """One cached token has 99% of the weight and value 0: the output is what the others,
+    each of a weight of 1 / (99 n) of that token's, add up to. More sequences (of the same
+    pages) than CTAs, so that hardly one is split into parts with maxima of their own.
+
+    Relative bound, all values being positive: half a bfloat16 step of the output (2^-8),
+    the weights' rounding to half with the largest scaled to 2^9 or more (2^-11, or half
+    of a subnormal step, 2^-25 of 2^9 / (99 n)), twice the error of the dominating score
+    s < 18 in nats ((D + 8) 2^-24 s, 4 * 2^-24 s and the query parts' 2^-17 s: one element
+    of the key is not 0), and float32 sums, 2^-11 as above.
+    """
+    B, page, width = 200, 128, -(-n // 128)
+    g = torch.Generator(device=DEV).manual_seed(n + T)
+    table = torch.randperm(width, generator=g, device=DEV).int().repeat(B, 1)
+    c = api.kv_cache(table, width, 1, page, D)
+    c.k_scale.fill_(1.0)
+    c.v_scale.fill_(0.5)
+    # 1 to 2 in steps of e4m3
+    c.v.copy_(1 + torch.randint(0, 9, c.v.shape, generator=g, device=DEV) / 8)
+    pid, slot = int(table[0, at // page]), at % page
+    c.k[pid, 0, slot, 0] = 16.0
+    c.v[pid, 0, slot] = 0.0
+    q, k, v = _new(B, T, G, 1, D, 90)
+    q.zero_()
+    q[..., 0] = math.log(99 * n) / 16
+    s = float(q[0, 0, 0, 0]) * 16  # as rounded
+    k.zero_()
+    k[..., 0] = -16.0  # the new tokens' weights are (99 n)^-2 of the dominating one's
+    ln = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    out = api.block_attention(q, k, v.abs(), c, ln, scale=1.0)
+    assert api.device_fault_flags() == 0
+    vals = (c.v[table[0].long(), 0].double() * 0.5).reshape(-1, D)[:n].sum(0)
+    off = out.double() / (vals / (math.exp(s) + (n - 1))) - 1
+    tol = 2.0 ** -8 + max(2.0 ** -11, 99 * n * 2.0 ** -34) + \
+        2 * 18 * ((D + 12) * 2.0 ** -24 + 2.0 ** -17) + 2.0 ** -11
+    assert float(off.abs().max()) <= tol
