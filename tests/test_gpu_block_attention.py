@@ -502,3 +502,35 @@ def test_a_dominating_token_of_value_zero(api, T, G, D, n, at):
     tol = 2.0 ** -8 + max(2.0 ** -11, 99 * n * 2.0 ** -34) + \
         2 * 18 * ((D + 12) * 2.0 ** -24 + 2.0 ** -17) + 2.0 ** -11
     assert float(off.abs().max()) <= tol
+
+
+@pytest.mark.parametrize("T,n,D,G", [(1000, 0, 128, 2), (1021, 4000, 64, 4), (4096, 0, 64, 1),
+                                     (4096, 4001, 128, 1)])
+def test_blocks_up_to_the_longest(api, T, n, D, G):
+    lens = [n, 17]
+    c = _cache(api, lens, max(1, -(-n // 64)), 1, 64, D, seed=100 + T)
+    q, k, v = _new(2, T, G, 1, D, 101 + n)
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    out = api.block_attention(q, k, v, c, ln)
+    assert api.device_fault_flags() == 0
+    _check_whole(out, q, k, v, c, lens)
+    # a tree that is one chain is the same block
+    chain = (torch.arange(T, device=DEV) - 1).int().repeat(2, 1)
+    assert torch.equal(api.block_attention(q, k, v, c, ln, parent=chain), out)
+
+
+def test_as_many_sequences_as_are_accepted(api):
+    B, page, D = 65535, 16, 64
+    g = torch.Generator(device=DEV).manual_seed(110)
+    c = api.kv_cache(torch.randint(0, 300, (B, 2), generator=g, device=DEV).int(), 300, 1, page, D)
+    for codes, scale in ((c.k, c.k_scale), (c.v, c.v_scale)):
+        codes.copy_((torch.randn(codes.shape, generator=g, device=DEV) * 90).clamp(-448, 448))
+        scale.fill_(2.0 ** -6)
+    q, k, v = _new(B, 1, 1, 1, D, 111)
+    lens = [b % 33 for b in range(B)]
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    out = api.block_attention(q, k, v, c, ln)
+    assert api.device_fault_flags() == 0
+    some = list(range(0, B, 997)) + [B - 2, B - 1]
+    sub = api.KvCache(c.k, c.v, c.k_scale, c.v_scale, c.page_table[some].contiguous())
+    _check_whole(out[some], q[some], k[some], v[some], sub, [lens[b] for b in some])

@@ -225,3 +225,14 @@ def test_whatever_the_workspace_holds(api, M, d_in, d_out, r):
         for a, b in zip(want, got):
             assert torch.equal(a, b), guess
     assert api.device_fault_flags() == 0
+
+
+@pytest.mark.parametrize("M,d_in,d_out,r,out", [(20011, 272, 1000, 16, "bf16"), (8192, 1024, 513, 128, "f32"),
+                                                (5, 4096, 151936, 128, "bf16")])
+def test_many_rows_and_many_columns(api, M, d_in, d_out, r, out):
+    t = {"bf16": torch.bfloat16, "f32": torch.float32}[out]
+    d = _inputs(M, d_in, d_out, r, seed=M)
+    gate = (torch.arange(M, device=DEV) % 3 != 0).to(torch.uint8)
+    y_ar, y_dr = api.dualpath_linear_int8(**d, gate=gate, out_dtype=t)
+    _check(y_ar, y_dr, d, t, gate)
+    assert api.device_fault_flags() == 0
