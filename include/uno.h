@@ -472,7 +472,8 @@ int uno_dualpath_linear_int8(const int8_t* x, const float* x_scale, const int8_t
  *               belong to one sequence each.
  * Limits: 0 <= B <= 65535, 0 <= T, n <= 2^20, 1 <= Hkv <= 1024, D 64 or 128,
  * page 16, 32, 64 or 128, width * page <= 2^30. k_new, v_new and the codes
- * 16-byte aligned. No workspace. Asynchronous on `stream`.
+ * 16-byte aligned. Where B, T, n, width or num_pages is 0 nothing is written (and the
+ * pointers may be null). No workspace. Asynchronous on `stream`.
  * ------------------------------------------------------------------------ */
 int uno_kv_append(const void* k_new, const void* v_new, const int32_t* start,
                   const int32_t* count, const int32_t* rows, int B, int T, int n, int Hkv, int D,

@@ -184,7 +184,8 @@ extern "C" int uno_kv_append(const void* k_new, const void* v_new, const int32_t
   // tokens touch at most this many pages of a sequence, whatever slot they start at
   const long long per_seq = n == 0 ? 0 : (n + page - 2) / page + 1;
   if (per_seq * B > 0x7FFFFFFFll) return UNO_ERR_SIZE;
-  if (B == 0 || n == 0 || T == 0) return UNO_OK;
+  // (of an empty pool or table no token is written, wherever it would go)
+  if (B == 0 || n == 0 || T == 0 || width == 0 || num_pages == 0) return UNO_OK;
   for (const void* p : {k_new, v_new, static_cast<const void*>(k_codes),
                         static_cast<const void*>(v_codes)}) {
     if (!p) return UNO_ERR_NULL;

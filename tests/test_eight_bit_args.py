@@ -117,3 +117,14 @@ def test_block_attention_args(lib):
     assert lib.uno_block_attention_workspace_bytes(64, 17, 32, 8, 128) > 0
     assert lib.uno_block_attention_workspace_bytes(64, 17, 33, 8, 128) == 0
     assert lib.uno_block_attention_workspace_bytes(64, 17, 32, 8, 96) == 0
+
+
+def test_an_append_to_an_empty_pool_or_table_writes_nothing(lib):
+    """Their tensors have no storage, so no pointers; the attention takes them too."""
+    def call(table, width, N, codes, scale):
+        return _name(lib.uno_kv_append(FAKE, FAKE, FAKE, None, None, 2, 4, 4, 2, 64, 16, table,
+                                       width, N, codes, codes, scale, scale, None))
+
+    assert call(None, 0, 6, FAKE, FAKE) == call(FAKE, 3, 0, None, None) == "UNO_OK"
+    assert call(None, 0, 0, None, None) == "UNO_OK"
+    assert call(None, 3, 6, FAKE, FAKE) == call(FAKE, 3, 6, None, FAKE) == "UNO_ERR_NULL"
