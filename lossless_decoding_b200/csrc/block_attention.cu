@@ -23,10 +23,10 @@
 // Products. tcgen05, rows on the 128 TMEM lanes. Scores: kind::f8f6f4 on the codes
 // as they are; the queries are split into two e4m3 parts, q 2^s = hi + lo
 // (bfloat16's 8 bits are two signed 4-bit halves; 2^s brings the row's largest
-// into [128, 256), and what e4m3's smallest step 2^-9 drops is below 2^-18 of it).
-// Weighted values: kind::f16, weights rounded to half (2^-11) as the A operand in
-// TMEM over the scores they came from (kHead says how they are scaled), values decoded to half in shared memory by
-// warps of their own (exact: e4m3 is a subset). With weights in e4m3 parts
+// into [128, 256), and half of e4m3's smallest step 2^-9, which is dropped, is at most
+// 2^-17 of it). Weighted values: kind::f16, weights rounded to half (2^-11; kHead says
+// how they are scaled) as the A operand in TMEM over the scores they came from, values
+// decoded to half in shared memory by warps of their own (exact: e4m3 is a subset). With weights in e4m3 parts
 // the decode would go, but splitting a weight costs the softmax warps more than
 // the decode costs (7 clocks an element against 1).
 //

@@ -80,8 +80,11 @@ constexpr int kFirstProducer = 6;
 constexpr int kProducers = 2;
 constexpr int kGemmThreads = (kFirstProducer + kProducers) * 32;
 constexpr int kInsert = 6;         // main K-blocks of the next tile before an adapter
-// int8: products take half the time, the y_ar drain before the adapter a little more
-// (1088 x 4096 -> 12288: 74 us with 6, 71 with 12, 68 with 18, 67 with 24)
+// int8: products take half the time, the y_ar drain before the adapter a little more.
+// A tile's K-blocks are the most there can be: with a short d_in the adapter follows the
+// whole next tile. us with 6, 12, 18, 24 and 32: 1088 x 4096 -> 12288 82, 79, 76, 76, 76;
+// 4096 x 4096 -> 12288 188, 175, 164, 160, 168; 1088 x 12288 -> 4096 75, 73, 72, 71, 71;
+// d_in of 1024 and 2048 within 3% of one another.
 constexpr int kInsertI8 = 24;
 constexpr int kPrefetch = 8;       // K-blocks of L2 prefetch ahead of the weight loads
 using dual_units::kMaxSplit;       // K-pieces of a split tile, at most
@@ -1078,7 +1081,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     // 64-column boxes from the warp's two staging boxes. Lanes hold rows, so direct
     // stores write 16-byte pieces of 32 rows at a time, and with the products twice as
     // fast as bf16's the epilogue sets the pace (1088 x 4096 -> 12288, both paths, calls
-    // back to back: 70 us through the boxes, 81 with direct stores).
+    // back to back: 70 us through the boxes, 81 with direct stores). TMA takes rows
+    // that are multiples of 16 bytes only, and float32 boxes would be twice as many:
+    // those go by direct stores (371 us at d_out 12289, 123 with float32 outputs, against 76).
     auto drain_tma = [&](uint32_t acc, int a0, int b0, const CUtensorMap* map, bool store,
                          bool from_f32, bool keep) {
       const uint32_t tq = acc + (static_cast<uint32_t>(quarter * 32) << 16);

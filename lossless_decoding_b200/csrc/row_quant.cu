@@ -8,8 +8,10 @@
 // Bound by HBM, and at 2 bytes in and 1 out nearly by issue slots: x (and the
 // residual) come in once, h and q go out once, a row stays in registers between
 // its loads and its stores, and an element costs few instructions (a rounding is
-// one fma onto 1.5 * 2^23, whose low byte is then the integer: 82 us against
-// 139 us of 8192 x 12288 with conversions to int). The row factor
+// one fma onto 1.5 * 2^23, whose low byte is then the integer). Measured, to
+// q: norm with residual 1 x 4096 6 us, 1088 x 4096 12 us, 8192 x 4096 57 us; quantiser
+// 8192 x 12288 46 us (6.6 TB/s). Widths that are not multiples of 8 go element by
+// element: 8192 x 4095 133 us (norm) and 76 us (quantiser, 23 us at 4096). The row factor
 // r = rsqrt(..) scales every |h w| alike, so max|y| = r max|h w| and
 // q = rint(h w * (127 / max|h w|)): the sum of squares and the maximum are one
 // block reduction, not two with the row read again between them.
